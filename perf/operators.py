@@ -116,7 +116,7 @@ def prepare(case, seed):
             st["valid"] = (torch.arange(S, device=DEV)[None, :] < n[:, None]).reshape(T).contiguous()
         st["losses"] = torch.empty(2, device=DEV)
         st["counts"] = torch.empty(G, E, dtype=torch.int32, device=DEV)
-        st["tokens"] = torch.empty(G, dtype=torch.int32, device=DEV)
+        st["tokens"] = torch.empty(G + 1, dtype=torch.int32, device=DEV)   # of each group, then of all
         st["grad_losses"] = torch.tensor([1e-2, 1e-3], device=DEV) * (1 + torch.rand(2, generator=g, device=DEV))
         st["dlogits"] = torch.empty_like(logits)
     elif case["op"] == "quantize":
@@ -153,16 +153,17 @@ def _balance(st):
     on = torch.ones(T, 1, device=DEV) if st["valid"] is None else st["valid"][:, None].float()
     counts = torch.zeros(G, E, dtype=torch.int32, device=DEV)
     counts.scatter_add_(1, st["ids"].view(G, -1).long(), on.int().expand(T, k).reshape(G, -1))
-    tokens = on.view(G, -1).sum(1).to(torch.int32)
+    valid = on.view(G, -1).sum(1, dtype=torch.int32)
+    tokens = torch.cat([valid, valid.sum(0, keepdim=True, dtype=torch.int32)])
     m = x.amax(1, keepdim=True)
     ex = torch.exp(x - m)
     total = ex.sum(1, keepdim=True)
     p, lse = ex / total, m + torch.log(total)
-    n = tokens.double().clamp_min(1)
+    n = valid.double().clamp_min(1)
     share = (p * on).view(G, -1, E).sum(1, dtype=torch.float64)
     f = counts.double() * (E / (k * n))[:, None]
     balance = ((f * share).sum(1) / n).sum() / G
-    z = (lse.square() * on).sum(dtype=torch.float64) / n.new_tensor(1.0).maximum(tokens.double().sum())
+    z = (lse.square() * on).sum(dtype=torch.float64) / tokens[-1].double().clamp_min(1)
     losses = torch.stack([balance, z]).float()
     if not st["step"]:
         return losses, counts, tokens
@@ -170,7 +171,7 @@ def _balance(st):
     per = lambda v: v.float()[:, None].expand(G, T // G).reshape(T, 1)   # noqa: E731
     ft = f.float()[:, None, :].expand(G, T // G, E).reshape(T, E)
     dot = (p * ft).sum(1, keepdim=True)
-    d = on * p * (gb * per(1 / (G * n)) * (ft - dot) + gz * (2 / tokens.sum().clamp_min(1).float()) * lse)
+    d = on * p * (gb * per(1 / (G * n)) * (ft - dot) + gz * (2 / tokens[-1].float().clamp_min(1)) * lse)
     return losses, counts, tokens, d.to(st["logits"].dtype)
 
 
@@ -288,7 +289,7 @@ def exact(case, seed):
                 d = gb / (G * max(1, n)) * (p * f - p * (p @ f)[:, None]) + 2 * gz / N * z[:, None] * p
                 grads.append(torch.where(on[:, None], d, torch.zeros_like(d)))
         got = (torch.tensor(losses, dtype=torch.float64, device=DEV), torch.stack(counts),
-               torch.tensor(tokens, dtype=torch.int32, device=DEV))
+               torch.tensor(tokens + [sum(tokens)], dtype=torch.int32, device=DEV))
         return got + (torch.cat(grads),) if case["step"] else got
     if case["op"] == "quantize":
         M, K = case["M"], case["K"]
