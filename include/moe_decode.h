@@ -276,6 +276,117 @@ int moe_decode_conventional_noalloc(const void *x, const int32_t *topk_ids, cons
                                     const uint8_t *w_down, const uint8_t *s_down,
                                     void *y_out, int B, int H, int I, int E, int k, void *stream);
 
+/* Training the router: per-expert counts, the balance loss and the z loss, and
+ * their gradient with respect to the router's logits.
+ *
+ * T tokens in G groups of S = T / G consecutive tokens (a group is the unit
+ * the balance loss is taken over: the whole batch, G = 1, or one sequence).
+ * Token t of group g is valid unless `valid` is given and valid[t] == 0.  With
+ * n_g the valid tokens of group g, c_ge the slots of its valid tokens routed to
+ * expert e, p_t = softmax(logits_t) and N = sum_g n_g:
+ *   losses[0] = 1/G sum_g E / (k n_g) * 1 / n_g * sum_e c_ge sum_t p_te
+ *   losses[1] = 1/N sum_t logsumexp(logits_t)^2
+ * (sums over valid tokens; a group without one contributes 0 to both, as does
+ * N = 0).  The counts are constants to the gradient:
+ *   dlogits_te = grad_losses[0] / (G n_g) * p_te (f_ge - sum_j f_gj p_tj)
+ *              + grad_losses[1] * 2/N * logsumexp(logits_t) * p_te,
+ *   f_ge = E c_ge / (k n_g);  0 for a token that is not valid.
+ *
+ *   logits       [T, E] of `dtype` (MOE_F32 or MOE_BF16), row t at t * ld elements
+ *   topk_ids     int32 [T, k]; ids outside [0, E) are not counted; a repeated
+ *                id counts as often as it stands there
+ *   valid        uint8 [T] or NULL (every token is valid)
+ *   losses       fp32 [2]
+ *   counts       int32 [G, E]
+ *   tokens       int32 [G + 1]: n_0 .. n_(G-1), then N
+ *   grad_losses  fp32 [2], device memory: the factors of the two losses
+ *   dlogits      [T, E] of `dtype`, row t at t * ld_d elements
+ * A logit of -inf (an expert ruled out) has probability 0; a valid row of -inf
+ * only has p = 0 and logsumexp taken as 0.  +inf and NaN give NaN.  The logits
+ * of a token that is not valid may hold anything.  Sums are FP32 over at most
+ * a few thousand tokens, then FP64, always in the same order: the same inputs
+ * give the same bits.  Elements between the rows (ld > E) are neither read
+ * nor written.
+ * Limits: E <= 1024, k <= 64 and k <= E, G divides T, T * k < 2^31,
+ * G <= 2^20, G * E < 2^28, strides up to 2^30.  `workspace` is device memory of at least
+ * moe_decode_balance_workspace() bytes, 256-byte aligned, used until the
+ * launches complete (calls that may overlap in time need one each); it need
+ * not be cleared.  T == 0 is a valid no-op that writes nothing. */
+#define MOE_F32 0
+#define MOE_BF16 1
+#define MOE_F16 2
+int moe_decode_balance_workspace(int T, int E, int k, int G, size_t *bytes);
+int moe_decode_balance(const void *logits, long long ld, int dtype, const int32_t *topk_ids, const uint8_t *valid,
+                       float *losses, int32_t *counts, int32_t *tokens, void *workspace, size_t workspace_bytes,
+                       int T, int E, int k, int G, void *stream);
+int moe_decode_balance_backward(const void *logits, long long ld, int dtype, const uint8_t *valid,
+                                const int32_t *counts, const int32_t *tokens, const float *grad_losses,
+                                void *dlogits, long long ld_d, int T, int E, int k, int G, void *stream);
+
+/* Rows to 8 bits with one scale for each block of 128: the operand of the
+ * products below.  For row m and block b of 128 columns (the last one may be
+ * shorter), with v the block's values:
+ *   scales[m, b] = max(amax |v| / 448, 2^-126),
+ *   q[m, c] = E4M3(v_c / scales[m, b])      round to nearest even
+ * amax over the block's finite values; both quotients are FP32 divisions,
+ * correctly rounded.  MOE_QUANT_POW2 raises each scale to the next power of two.
+ * A NaN or an infinity becomes the NaN code 0x7F and leaves its block's other
+ * values as they would be without it.
+ *   x       [M, K] of `dtype` (MOE_F32, MOE_BF16 or MOE_F16), row m at m * ldx elements;
+ *           with MOE_QUANT_SWIGLU [M, 2K] and v_c = SiLU(x[m, c]) * x[m, K + c]
+ *           in FP32, not rounded before the quantisation
+ *   q       uint8 [M, K] E4M3 codes
+ *   scales  fp32 [M, ceil(K / 128)]
+ * Limits: M * ceil(K / 128) < 2^30, ldx up to 2^30.  M == 0 is a valid no-op. */
+#define MOE_QUANT_SWIGLU 1
+#define MOE_QUANT_POW2 2
+int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q, float *scales,
+                            int M, int K, int flags, void *stream);
+
+/* Products of 8-bit operands with a scale for each block of 128:
+ *   y[m, n] = sum_b sx[m, b] * sw[n / 128, b] * sum_{c in block b} x[m, c] * w[n, c]
+ * with each block's sum formed on the matrix cores, scaled and added in FP32,
+ * and one rounding to y.  For an FP32 y the block's sum is FP32 too.  For a
+ * 16-bit y it may be what the FP8 matrix instruction keeps, which adds eight
+ * products at a time and cuts them off 2^-13 below the largest: 1.5e-5 of the
+ * sum's root mean square on normally distributed codes, far below a 16-bit
+ * result's half step, and at most 2^-10 of the sum of the products' magnitudes.
+ *   x   uint8 [M, K] E4M3 codes, row m at m * ldx bytes
+ *   sx  fp32 [M, ceil(K / 128)]
+ *   w   uint8 [N, K] E4M3 codes
+ *   sw  fp32 [ceil(N / 128), ceil(K / 128)]
+ *   y   [M, N] of y_dtype (MOE_F32, MOE_BF16 or MOE_F16), row m at m * ldy elements
+ * K a multiple of 16, x and w 16-byte aligned, ldx a multiple of 16.  The
+ * gradient with respect to x is the same product with w and sw transposed.
+ *
+ * moe_decode_matmul_fp8_experts: the same for E matrices w [E, N, K], sw [E,
+ * ceil(N / 128), ceil(K / 128)] on rows sorted by expert: the first counts[0]
+ * rows of y belong to expert 0, the next counts[1] to expert 1, and so on
+ * (counts int32 [E], device memory: moe_decode_balance's with G = 1).  Row m
+ * of y comes from row m of x, or from row x_rows[m] where x_rows (int32 [M])
+ * is given; x and sx have X rows.  A row number outside [0, X) is not read
+ * through: its row of y is NaN.  Rows of y behind the last expert's are left
+ * as they were; negative counts are taken as 0, and rows beyond M are not
+ * computed.
+ * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts), and with x_rows
+ * X * ldx < 2^32.  M == 0 is a valid no-op.
+ *
+ * The _ex forms take the kernel variant (0 = the built-in choice, which
+ * moe_decode_matmul_fp8_plan reports; E = 0 asks about one matrix). */
+#define MOE_MATMUL_TILE_64 1
+int moe_decode_matmul_fp8(const uint8_t *x, long long ldx, const float *sx, const uint8_t *w, const float *sw,
+                          void *y, long long ldy, int y_dtype, int M, int N, int K, void *stream);
+int moe_decode_matmul_fp8_ex(const uint8_t *x, long long ldx, const float *sx, const uint8_t *w, const float *sw,
+                             void *y, long long ldy, int y_dtype, int M, int N, int K, int variant, void *stream);
+int moe_decode_matmul_fp8_experts(const uint8_t *x, long long ldx, const float *sx, const int32_t *x_rows,
+                                  const int32_t *counts, const uint8_t *w, const float *sw,
+                                  void *y, long long ldy, int y_dtype, int X, int M, int N, int K, int E, void *stream);
+int moe_decode_matmul_fp8_experts_ex(const uint8_t *x, long long ldx, const float *sx, const int32_t *x_rows,
+                                     const int32_t *counts, const uint8_t *w, const float *sw,
+                                     void *y, long long ldy, int y_dtype, int X, int M, int N, int K, int E,
+                                     int variant, void *stream);
+int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int *variant, int *workgroups);
+
 /* Bandwidth probes that set the denominator of the efficiency figure (blog
  * post, "Hardware efficiency": peak measured with a copy kernel over
  * contiguous memory).  copy: dst[0:bytes) = src[0:bytes); read: reads

@@ -32,11 +32,20 @@ MOE_GATE_UP_EXPERT_GROUPED_MFMA = 3
 MOE_DOWN_PER_TOKEN = 1
 MOE_DOWN_EXPERT_GROUPED = 2
 MOE_DOWN_EXPERT_GROUPED_MFMA = 3
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_F16 = 2
+MOE_QUANT_SWIGLU = 1
+MOE_QUANT_POW2 = 2
+MOE_MATMUL_TILE_64 = 1
 
 EXPORTS = (
     "moe_decode_gate_up", "moe_decode_down", "moe_decode_gate_up_ex", "moe_decode_down_ex",
     "moe_decode_gate_up_plan", "moe_decode_down_plan", "moe_decode_conventional_workspace",
     "moe_decode_conventional", "moe_decode_conventional_noalloc", "moe_decode_route", "moe_decode_gate_up_routed", "moe_decode_gate_up_routed_ex",
+    "moe_decode_balance_workspace", "moe_decode_balance", "moe_decode_balance_backward", "moe_decode_quantize_fp8",
+    "moe_decode_matmul_fp8", "moe_decode_matmul_fp8_ex", "moe_decode_matmul_fp8_experts",
+    "moe_decode_matmul_fp8_experts_ex", "moe_decode_matmul_fp8_plan",
     "moe_decode_copy_peak", "moe_decode_read_peak",
     "moe_decode_strerror",
 )
@@ -73,6 +82,16 @@ def lib() -> ctypes.CDLL:
             L.moe_decode_route.argtypes = [P] * 3 + [I] * 3 + [P]
             L.moe_decode_gate_up_routed.argtypes = [P] * 9 + [I] * 5 + [P]
             L.moe_decode_gate_up_routed_ex.argtypes = [P] * 9 + [I] * 7 + [P]
+            LL = ctypes.c_longlong
+            L.moe_decode_balance_workspace.argtypes = [I] * 4 + [ctypes.POINTER(S)]
+            L.moe_decode_balance.argtypes = [P, LL, I] + [P] * 6 + [S] + [I] * 4 + [P]
+            L.moe_decode_balance_backward.argtypes = [P, LL, I] + [P] * 5 + [LL] + [I] * 4 + [P]
+            L.moe_decode_quantize_fp8.argtypes = [P, LL, I, P, P, I, I, I, P]
+            L.moe_decode_matmul_fp8.argtypes = [P, LL, P, P, P, P, LL] + [I] * 4 + [P]
+            L.moe_decode_matmul_fp8_ex.argtypes = [P, LL, P, P, P, P, LL] + [I] * 5 + [P]
+            L.moe_decode_matmul_fp8_experts.argtypes = [P, LL] + [P] * 6 + [LL] + [I] * 6 + [P]
+            L.moe_decode_matmul_fp8_experts_ex.argtypes = [P, LL] + [P] * 6 + [LL] + [I] * 7 + [P]
+            L.moe_decode_matmul_fp8_plan.argtypes = [I] * 4 + [IP, IP]
             L.moe_decode_copy_peak.argtypes = [P, P, S, P]
             L.moe_decode_read_peak.argtypes = [P, S, P, P]
             L.moe_decode_strerror.argtypes = [I]
@@ -275,6 +294,186 @@ def moe_decode_conventional_noalloc(x, topk_ids, topk_weights, w_gate, s_gate, w
     if rc:
         raise MoeDecodeError(rc, "moe_decode_conventional_noalloc")
     return y_out
+
+
+# ---------------------------------------------------------------- router training and block-scaled 8-bit products
+_codes = None
+
+
+def _dtype_code(t, name, allowed):
+    """MOE_F32 / MOE_BF16 / MOE_F16 of a tensor; 16-bit integer tensors hold bf16 patterns."""
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.uint16: MOE_BF16,
+                  torch.float16: MOE_F16}
+    c = _codes.get(t.dtype)
+    if c is None or c not in allowed:
+        raise ValueError(f"{name} has dtype {t.dtype}, which this call does not take")
+    return c
+
+
+def _rows(t, name, rows=None, cols=None):
+    """Row stride of a GPU matrix whose rows are contiguous (the rows themselves may lie apart)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    ld, one = t.stride()
+    if one != 1 and t.shape[1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return ld if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _flat(t, name, numel, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(where, fn, stream, tensors, *args):
+    """fn(*args, stream) on the device that holds `tensors`: on its current stream where none is given."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc:
+        raise MoeDecodeError(rc, where)
+
+
+def moe_decode_balance_workspace(T, E, k, G=1):
+    """Bytes of device workspace moe_decode_balance needs."""
+    n = ctypes.c_size_t()
+    rc = lib().moe_decode_balance_workspace(T, E, k, G, ctypes.byref(n))
+    if rc:
+        raise MoeDecodeError(rc, "moe_decode_balance_workspace")
+    return n.value
+
+
+def moe_decode_balance(logits, topk_ids, losses, counts, tokens, valid=None, workspace=None, stream=None):
+    """Per-expert counts [G,E], valid tokens [G+1], and the balance and z losses [2] of the router's
+    logits [T,E] (fp32 or bf16) and choices topk_ids [T,k] (see include/moe_decode.h).
+
+    valid: [T] bool or uint8, the tokens that count.  Without a workspace one is taken from torch's
+    allocator for the call (which then runs on the current stream)."""
+    import torch
+    T, E = logits.shape
+    k, G = topk_ids.shape[-1], counts.shape[0]
+    dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
+    args = (logits.data_ptr(), _rows(logits, "logits"), dt, _flat(topk_ids, "topk_ids", T * k, torch.int32),
+            None if valid is None else _flat(valid, "valid", T, (torch.bool, torch.uint8)),
+            _flat(losses, "losses", 2, torch.float32), _flat(counts, "counts", G * E, torch.int32),
+            _flat(tokens, "tokens", G + 1, torch.int32))
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("moe_decode_balance on a given stream needs a workspace")
+        workspace = torch.empty(moe_decode_balance_workspace(T, E, k, G), dtype=torch.uint8, device=logits.device)
+    _call("moe_decode_balance", lib().moe_decode_balance, stream,
+          (logits, topk_ids, valid, losses, counts, tokens, workspace), *args,
+          _flat(workspace, "workspace", workspace.numel(), torch.uint8), workspace.numel(), T, E, k, G)
+    return losses, counts, tokens
+
+
+def moe_decode_balance_backward(logits, counts, tokens, grad_losses, dlogits, k, valid=None, stream=None):
+    """dlogits [T,E] = the gradient of grad_losses . losses of moe_decode_balance with respect to the logits, from
+    the counts and tokens that call left (see include/moe_decode.h)."""
+    import torch
+    T, E = logits.shape
+    G = counts.shape[0]
+    dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
+    if _dtype_code(dlogits, "dlogits", (MOE_F32, MOE_BF16)) != dt:
+        raise ValueError("dlogits must have the type of logits")
+    _call("moe_decode_balance_backward", lib().moe_decode_balance_backward, stream,
+          (logits, valid, counts, tokens, grad_losses, dlogits),
+          logits.data_ptr(), _rows(logits, "logits"), dt,
+          None if valid is None else _flat(valid, "valid", T, (torch.bool, torch.uint8)),
+          _flat(counts, "counts", G * E, torch.int32), _flat(tokens, "tokens", G + 1, torch.int32),
+          _flat(grad_losses, "grad_losses", 2, torch.float32), dlogits.data_ptr(), _rows(dlogits, "dlogits", T, E),
+          T, E, k, G)
+    return dlogits
+
+
+def moe_decode_quantize_fp8(x, q, scales, swiglu=False, pow2=False, stream=None):
+    """q [M,K] E4M3 codes (uint8) and scales fp32 [M, ceil(K/128)] of x [M,K], or with swiglu of
+    SiLU(x[:, :K]) * x[:, K:] of x [M,2K]; pow2: scales are powers of two (see include/moe_decode.h)."""
+    import torch
+    M, K = q.shape
+    dt = _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16))
+    _call("moe_decode_quantize_fp8", lib().moe_decode_quantize_fp8, stream, (x, q, scales),
+          x.data_ptr(), _rows(x, "x", M, 2 * K if swiglu else K), dt, _flat(q, "q", M * K, torch.uint8),
+          _flat(scales, "scales", M * -(-K // 128), torch.float32), M, K,
+          (MOE_QUANT_SWIGLU if swiglu else 0) | (MOE_QUANT_POW2 if pow2 else 0))
+    return q, scales
+
+
+def _codes_rows(x, name, rows=None, cols=None):
+    import torch
+    if x.dtype != torch.uint8:
+        raise ValueError(f"{name} has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
+    return _rows(x, name, rows, cols)
+
+
+def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None):
+    """y [M,N] = the product of x [M,K] and w [N,K] (E4M3 codes, uint8) with scales sx [M, ceil(K/128)] and
+    sw [ceil(N/128), ceil(K/128)] (see include/moe_decode.h)."""
+    import torch
+    M, K = x.shape
+    N = w.shape[0]
+    kb = -(-K // 128)
+    args = (x.data_ptr(), _codes_rows(x, "x"), _flat(sx, "sx", M * kb, torch.float32),
+            _flat(w, "w", N * K, torch.uint8), _flat(sw, "sw", -(-N // 128) * kb, torch.float32),
+            y.data_ptr(), _rows(y, "y", M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), M, N, K)
+    if variant is None:
+        _call("moe_decode_matmul_fp8", lib().moe_decode_matmul_fp8, stream, (x, sx, w, sw, y), *args)
+    else:
+        _call("moe_decode_matmul_fp8", lib().moe_decode_matmul_fp8_ex, stream, (x, sx, w, sw, y), *args, int(variant))
+    return y
+
+
+def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=None, variant=None):
+    """The product of moe_decode_matmul_fp8 for E matrices w [E,N,K] on rows sorted by expert, counts [E] (int32) of
+    them each; x_rows [M] (int32): the row of x that each row of y comes from (see include/moe_decode.h)."""
+    import torch
+    X, K = x.shape
+    E, N = w.shape[0], w.shape[1]
+    M = y.shape[0]
+    kb = -(-K // 128)
+    args = (x.data_ptr(), _codes_rows(x, "x"), _flat(sx, "sx", X * kb, torch.float32),
+            None if x_rows is None else _flat(x_rows, "x_rows", M, torch.int32),
+            _flat(counts, "counts", E, torch.int32),
+            _flat(w, "w", E * N * K, torch.uint8), _flat(sw, "sw", E * -(-N // 128) * kb, torch.float32),
+            y.data_ptr(), _rows(y, "y", M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), X, M, N, K, E)
+    tensors = (x, sx, x_rows, counts, w, sw, y)
+    if variant is None:
+        _call("moe_decode_matmul_fp8_experts", lib().moe_decode_matmul_fp8_experts, stream, tensors, *args)
+    else:
+        _call("moe_decode_matmul_fp8_experts", lib().moe_decode_matmul_fp8_experts_ex, stream, tensors, *args, int(variant))
+    return y
+
+
+def moe_decode_matmul_fp8_plan(M, N, K, E=0):
+    """(variant, workgroups) the built-in choice for these sizes (E = 0: one matrix)."""
+    v, g = ctypes.c_int(), ctypes.c_int()
+    rc = lib().moe_decode_matmul_fp8_plan(M, N, K, E, ctypes.byref(v), ctypes.byref(g))
+    if rc:
+        raise MoeDecodeError(rc, "moe_decode_matmul_fp8_plan")
+    return v.value, g.value
 
 
 def moe_decode_copy_peak(src, dst, stream=None):

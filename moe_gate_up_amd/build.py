@@ -15,6 +15,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 # with the measurements, in csrc/host.hpp).
 SOURCES = [
     ("moe_decode.hip", []),
+    ("balance.hip", []),
+    ("block_fp8.hip", []),
     ("down_token.hip", ["-mllvm", "-amdgpu-sched-strategy=max-memory-clause"]),
     ("down_mfma.hip", ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]),
 ]

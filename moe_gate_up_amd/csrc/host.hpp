@@ -31,6 +31,13 @@ constexpr int kMaxDevices = 64;
 // + R scales + h (8 VGPRs).
 constexpr bool down_fits(int np, int r) { return np * (5 * r + 8) <= 224; }
 
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
 // Runs f() once per device, on the first call made with that device current,
 // and returns its result on every call.
 struct PerDeviceOnce {

@@ -19,20 +19,15 @@
 
 namespace {
 
+using moe_host::aligned;
 using moe_host::DownLaunch;
 using moe_host::kLdsPerCu;
 using moe_host::kMaxDevices;
 using moe_host::kMaxDownPasses;
 using moe_host::kWavesPerBlock;
+using moe_host::overlaps;
 using moe_host::PerDeviceOnce;
 constexpr int kMaxGateUpPasses = 8;   // H <= 8 passes of 1024 elements = 8192
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
 
 int check_shape(int B, int H, int I, int E, int k) {
   if (B < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || k > E) return MOE_ERR_SHAPE;

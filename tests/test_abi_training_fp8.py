@@ -1,0 +1,170 @@
+"""Host-side checks of the router training and block-scaled 8-bit calls of the C
+ABI (CPU only: every case returns during argument validation, before any HIP
+call; the pointers are addresses that are never dereferenced)."""
+import ctypes
+
+import pytest
+
+import moe_gate_up_amd as mg
+
+A = 0x100000000000   # aligned stand-ins for device buffers, 64 GiB apart
+S = 0x1000000000
+
+
+def at(i, plus=0):
+    return A + i * S + plus
+
+
+def P(v):
+    return ctypes.c_void_p(v or None)
+
+
+def balance(logits=at(0), ld=128, dtype=mg.MOE_F32, ids=at(1), valid=0, losses=at(2), counts=at(3), tokens=at(4),
+            ws=at(5), ws_bytes=None, T=64, E=128, k=8, G=1):
+    if ws_bytes is None:
+        n = ctypes.c_size_t()
+        mg.lib().moe_decode_balance_workspace(T, E, k, G, ctypes.byref(n))   # leaves 0 where it refuses
+        ws_bytes = n.value
+    return mg.lib().moe_decode_balance(P(logits), ld, dtype, P(ids), P(valid), P(losses), P(counts), P(tokens), P(ws),
+                                       ws_bytes, T, E, k, G, None)
+
+
+def backward(logits=at(0), ld=128, dtype=mg.MOE_F32, valid=0, counts=at(1), tokens=at(2), grad=at(3), d=at(4), ld_d=128,
+             T=64, E=128, k=8, G=1):
+    return mg.lib().moe_decode_balance_backward(P(logits), ld, dtype, P(valid), P(counts), P(tokens), P(grad), P(d), ld_d,
+                                                T, E, k, G, None)
+
+
+def quantize(x=at(0), ldx=2048, dtype=mg.MOE_BF16, q=at(1), s=at(2), M=32, K=2048, flags=0):
+    return mg.lib().moe_decode_quantize_fp8(P(x), ldx, dtype, P(q), P(s), M, K, flags, None)
+
+
+def matmul(x=at(0), ldx=2048, sx=at(1), w=at(2), sw=at(3), y=at(4), ldy=4096, dtype=mg.MOE_BF16, M=32, N=4096, K=2048,
+           variant=None):
+    args = [P(x), ldx, P(sx), P(w), P(sw), P(y), ldy, dtype, M, N, K]
+    if variant is None:
+        return mg.lib().moe_decode_matmul_fp8(*args, None)
+    return mg.lib().moe_decode_matmul_fp8_ex(*args, variant, None)
+
+
+def experts(x=at(0), ldx=2048, sx=at(1), rows=at(5), counts=at(6), w=at(2), sw=at(3), y=at(4), ldy=1536,
+            dtype=mg.MOE_BF16, X=32, M=256, N=1536, K=2048, E=128, variant=None):
+    args = [P(x), ldx, P(sx), P(rows), P(counts), P(w), P(sw), P(y), ldy, dtype, X, M, N, K, E]
+    if variant is None:
+        return mg.lib().moe_decode_matmul_fp8_experts(*args, None)
+    return mg.lib().moe_decode_matmul_fp8_experts_ex(*args, variant, None)
+
+
+@pytest.mark.parametrize("fn", [balance, backward])
+def test_balance_shapes(fn):
+    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=65, E=128), dict(k=9, E=8, ld=8), dict(E=1025, ld=1025), dict(G=0),
+                dict(G=5), dict(ld=127), dict(T=1 << 30, k=2), dict(T=1 << 21, G=1 << 21), dict(T=1 << 19, G=1 << 19, E=512, ld=512),
+                dict(ld=(1 << 30) + 128)):
+        if fn is backward and "ld" in bad:
+            bad.setdefault("ld_d", max(bad["ld"], 0))
+        assert fn(**bad) == mg.MOE_ERR_SHAPE, bad
+    assert fn(dtype=mg.MOE_F16) == mg.MOE_ERR_ARG
+    assert fn(dtype=7) == mg.MOE_ERR_ARG
+
+
+def test_balance_pointers():
+    for n in ("logits", "ids", "losses", "counts", "tokens", "ws"):
+        assert balance(**{n: 0}) == mg.MOE_ERR_NULL, n
+    for n, off in (("logits", 2), ("ids", 2), ("losses", 1), ("counts", 2), ("tokens", 3), ("ws", 128)):
+        assert balance(**{n: at(8, off)}) == mg.MOE_ERR_ALIGN, n
+    assert balance(logits=at(8, 1), dtype=mg.MOE_BF16) == mg.MOE_ERR_ALIGN
+    for n in ("logits", "counts", "tokens", "grad", "d"):
+        assert backward(**{n: 0}) == mg.MOE_ERR_NULL, n
+    for n, off in (("logits", 2), ("counts", 2), ("tokens", 3), ("grad", 1), ("d", 2)):
+        assert backward(**{n: at(8, off)}) == mg.MOE_ERR_ALIGN, n
+
+
+def test_balance_overlaps():
+    assert balance(counts=at(0, 64)) == mg.MOE_ERR_ALIAS
+    assert balance(losses=at(1, 64)) == mg.MOE_ERR_ALIAS
+    assert balance(valid=at(4)) == mg.MOE_ERR_ALIAS
+    assert balance(tokens=at(3, 508)) == mg.MOE_ERR_ALIAS       # the last count
+    assert balance(ws=at(0)) == mg.MOE_ERR_ALIAS
+    assert balance(ws_bytes=64) == mg.MOE_ERR_ARG
+    assert backward(d=at(0, 16)) == mg.MOE_ERR_ALIAS
+    assert backward(d=at(1)) == mg.MOE_ERR_ALIAS
+    assert backward(valid=at(4, 100)) == mg.MOE_ERR_ALIAS
+
+
+def test_empty_calls_do_nothing():
+    assert balance(T=0, logits=0, ids=0, losses=0, counts=0, tokens=0, ws=0) == mg.MOE_OK
+    assert backward(T=0, logits=0, counts=0, tokens=0, grad=0, d=0) == mg.MOE_OK
+    assert quantize(M=0, x=0, q=0, s=0) == mg.MOE_OK
+    assert matmul(M=0, x=0, sx=0, w=0, sw=0, y=0) == mg.MOE_OK
+    assert experts(M=0, X=0, x=0, sx=0, rows=0, counts=0, w=0, sw=0, y=0) == mg.MOE_OK
+    assert mg.moe_decode_balance_workspace(0, 128, 8) == 0
+
+
+def test_quantize_refusals():
+    for bad in (dict(M=-1), dict(K=0), dict(K=-16), dict(ldx=2047), dict(flags=mg.MOE_QUANT_SWIGLU), dict(M=1 << 26),
+                dict(ldx=(1 << 30) + 1), dict(K=(1 << 28) + 1, ldx=1 << 29)):
+        assert quantize(**bad) == mg.MOE_ERR_SHAPE, bad       # SwiGLU: a row of x is 2 K long
+    assert quantize(flags=4) == mg.MOE_ERR_ARG
+    assert quantize(flags=-1) == mg.MOE_ERR_ARG
+    assert quantize(dtype=3) == mg.MOE_ERR_ARG
+    for n in ("x", "q", "s"):
+        assert quantize(**{n: 0}) == mg.MOE_ERR_NULL
+    assert quantize(x=at(8, 1)) == mg.MOE_ERR_ALIGN
+    assert quantize(x=at(8, 2), dtype=mg.MOE_F32) == mg.MOE_ERR_ALIGN
+    assert quantize(s=at(8, 2)) == mg.MOE_ERR_ALIGN
+    assert quantize(q=at(0, 4096)) == mg.MOE_ERR_ALIAS
+    assert quantize(s=at(1, 65532)) == mg.MOE_ERR_ALIAS
+    assert quantize(s=at(0, 131068)) == mg.MOE_ERR_ALIAS
+
+
+@pytest.mark.parametrize("fn", [matmul, experts])
+def test_matmul_refusals(fn):
+    for bad in (dict(M=-1), dict(N=0), dict(K=0), dict(K=2040), dict(ldx=2032), dict(ldx=2056), dict(ldy=100),
+                dict(N=1 << 20, ldy=1 << 20), dict(ldx=(1 << 30) + 16), dict(ldy=(1 << 30) + 4)):
+        assert fn(**bad) == mg.MOE_ERR_SHAPE, bad
+    assert fn(dtype=3) == mg.MOE_ERR_ARG
+    assert fn(variant=99) == mg.MOE_ERR_ARG
+    assert fn(variant=-1) == mg.MOE_ERR_ARG
+    for n in ("x", "sx", "w", "sw", "y"):
+        assert fn(**{n: 0}) == mg.MOE_ERR_NULL, n
+    for n, off in (("x", 8), ("w", 8), ("sx", 2), ("sw", 2), ("y", 1)):
+        assert fn(**{n: at(8, off)}) == mg.MOE_ERR_ALIGN, n
+    assert fn(y=at(8, 2), dtype=mg.MOE_F32) == mg.MOE_ERR_ALIGN
+    for i in range(4):
+        assert fn(y=at(i, 16)) == mg.MOE_ERR_ALIAS, i
+
+
+def test_experts_refusals():
+    assert experts(counts=0) == mg.MOE_ERR_NULL
+    assert experts(counts=at(8, 2)) == mg.MOE_ERR_ALIGN
+    assert experts(rows=at(8, 2)) == mg.MOE_ERR_ALIGN
+    assert experts(y=at(5)) == mg.MOE_ERR_ALIAS
+    assert experts(y=at(6)) == mg.MOE_ERR_ALIAS
+    for bad in (dict(E=0), dict(E=1025), dict(M=1 << 24), dict(X=-1), dict(X=0), dict(rows=0, X=255),
+                dict(X=1 << 21)):   # 2^21 rows of 2048 bytes to pick from: offsets pass 32 bits
+        assert experts(**bad) == mg.MOE_ERR_SHAPE, bad
+
+
+def test_plan_names_a_variant():
+    for M, N, K, E in ((1, 4096, 2048, 0), (8192, 4096, 4096, 0), (256, 1536, 2048, 128), (32768, 1536, 2048, 128), (0, 128, 128, 0)):
+        v, g = mg.moe_decode_matmul_fp8_plan(M, N, K, E)
+        assert v >= 1 and g >= 0
+    with pytest.raises(mg.MoeDecodeError):
+        mg.moe_decode_matmul_fp8_plan(1, 128, 100)
+
+
+def test_binding_refuses_cpu_tensors():
+    import torch
+    f = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(ValueError):
+        mg.moe_decode_balance(f(4, 8), f(4, 2, **i32), f(2), f(1, 8, **i32), f(2, **i32))
+    with pytest.raises(ValueError):
+        mg.moe_decode_balance_backward(f(4, 8), f(1, 8, **i32), f(2, **i32), f(2), f(4, 8), 2)
+    u8 = dict(dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        mg.moe_decode_quantize_fp8(f(4, 128), f(4, 128, **u8), f(4, 1))
+    with pytest.raises(ValueError):
+        mg.moe_decode_matmul_fp8(f(4, 128, **u8), f(4, 1), f(8, 128, **u8), f(1, 1), f(4, 8))
+    with pytest.raises(ValueError):
+        mg.moe_decode_matmul_fp8_experts(f(4, 128, **u8), f(4, 1), f(2, **i32), f(2, 8, 128, **u8), f(2, 1, 1), f(4, 8))
