@@ -368,12 +368,26 @@ int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q,
  * through: its row of y is NaN.  Rows of y behind the last expert's are left
  * as they were; negative counts are taken as 0, and rows beyond M are not
  * computed.
- * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts), and with x_rows
- * X * ldx < 2^32.  M == 0 is a valid no-op.
+ * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts), strides up to 2^30.
+ * M == 0 is a valid no-op.
  *
- * The _ex forms take the kernel variant (0 = the built-in choice, which
- * moe_decode_matmul_fp8_plan reports; E = 0 asks about one matrix). */
-#define MOE_MATMUL_TILE_64 1
+ * Kernel variants (the _ex forms take one; 0 = the built-in choice, the
+ * fastest measured; moe_decode_matmul_fp8_plan reports it for a 16-bit y and
+ * ordinary strides, E = 0 asking about one matrix):
+ *   MOE_MATMUL_ROWS_16: 16 rows a workgroup, its wavefronts sharing out K.
+ *   MOE_MATMUL_TILE_<rows>X<columns>: a tile of y a workgroup, both operands
+ *     through LDS; _STREAM reads w as data that is used once.
+ *   MOE_MATMUL_FAR_ROWS: as TILE_64X64 for any stride.
+ * A TILE variant needs 32-bit offsets to reach its rows of x (with x_rows all X
+ * rows), TILE_256X256 a 16-bit y: MOE_ERR_ARG otherwise.  For a 16-bit y the
+ * TILE and FAR variants sum on the FP8 matrix instruction, ROWS_16 in FP32. */
+#define MOE_MATMUL_ROWS_16 1
+#define MOE_MATMUL_TILE_64X64 2
+#define MOE_MATMUL_TILE_64X128 3
+#define MOE_MATMUL_TILE_64X128_STREAM 4
+#define MOE_MATMUL_TILE_128X128 5
+#define MOE_MATMUL_TILE_256X256 6
+#define MOE_MATMUL_FAR_ROWS 7
 int moe_decode_matmul_fp8(const uint8_t *x, long long ldx, const float *sx, const uint8_t *w, const float *sw,
                           void *y, long long ldy, int y_dtype, int M, int N, int K, void *stream);
 int moe_decode_matmul_fp8_ex(const uint8_t *x, long long ldx, const float *sx, const uint8_t *w, const float *sw,

@@ -37,7 +37,13 @@ MOE_BF16 = 1
 MOE_F16 = 2
 MOE_QUANT_SWIGLU = 1
 MOE_QUANT_POW2 = 2
-MOE_MATMUL_TILE_64 = 1
+MOE_MATMUL_ROWS_16 = 1
+MOE_MATMUL_TILE_64X64 = 2
+MOE_MATMUL_TILE_64X128 = 3
+MOE_MATMUL_TILE_64X128_STREAM = 4
+MOE_MATMUL_TILE_128X128 = 5
+MOE_MATMUL_TILE_256X256 = 6
+MOE_MATMUL_FAR_ROWS = 7
 
 EXPORTS = (
     "moe_decode_gate_up", "moe_decode_down", "moe_decode_gate_up_ex", "moe_decode_down_ex",
@@ -297,61 +303,76 @@ def moe_decode_conventional_noalloc(x, topk_ids, topk_weights, w_gate, s_gate, w
 
 
 # ---------------------------------------------------------------- router training and block-scaled 8-bit products
-_codes = None
+_torch = None   # the module and what is looked up in it once, by _load()
+_codes = {}     # tensor type -> MOE_F32 / MOE_BF16 / MOE_F16; 16-bit integer tensors hold bf16 patterns
+
+
+def _load():
+    """The library, with torch's lookups done once: a small call costs more on the host than on the GPU."""
+    global _torch, _u8, _i32, _f32, _flags, _raw_stream, _raw_device
+    if _torch is None:
+        import torch
+        _codes.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16,
+                       torch.uint16: MOE_BF16, torch.float16: MOE_F16})
+        _u8, _i32, _f32, _flags = torch.uint8, torch.int32, torch.float32, (torch.bool, torch.uint8)
+        # the current stream's handle and the current device without a Python object around them
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _torch = torch
+    return _lib or lib()
 
 
 def _dtype_code(t, name, allowed):
-    """MOE_F32 / MOE_BF16 / MOE_F16 of a tensor; 16-bit integer tensors hold bf16 patterns."""
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.uint16: MOE_BF16,
-                  torch.float16: MOE_F16}
     c = _codes.get(t.dtype)
     if c is None or c not in allowed:
         raise ValueError(f"{name} has dtype {t.dtype}, which this call does not take")
     return c
 
 
-def _rows(t, name, rows=None, cols=None):
-    """Row stride of a GPU matrix whose rows are contiguous (the rows themselves may lie apart)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+def _rows(t, name, device, rows, cols):
+    """Row stride of a GPU matrix [rows, cols] whose rows are contiguous (they may lie apart)."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if rows < 2 or cols < 2:
+        ld, one = t.stride()
+        if one != 1 and cols > 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        return ld if rows > 1 else cols
     ld, one = t.stride()
-    if one != 1 and t.shape[1] != 1:
+    if one != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return ld if t.shape[0] > 1 else max(t.shape[1], 1)
+    return ld
 
 
-def _flat(t, name, numel, dtype):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
+def _flat(t, name, device, numel, dtype):
+    """Address of a contiguous GPU tensor of that many elements."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
+    if t.dtype is not dtype and (dtype is not _flags or t.dtype not in _flags):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {numel} contiguous elements, got shape {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
 
-def _call(where, fn, stream, tensors, *args):
-    """fn(*args, stream) on the device that holds `tensors`: on its current stream where none is given."""
-    import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-    if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+def _gpu(t, name):
+    """The GPU that holds `t`."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return i
+
+
+def _call(where, fn, device, stream, *args):
+    """fn(*args, stream) with the GPU `device` current: on its current stream where none is given."""
+    s = _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    if device == _raw_device():
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(device):
             rc = fn(*args, s)
     if rc:
         raise MoeDecodeError(rc, where)
@@ -372,39 +393,38 @@ def moe_decode_balance(logits, topk_ids, losses, counts, tokens, valid=None, wor
 
     valid: [T] bool or uint8, the tokens that count.  Without a workspace one is taken from torch's
     allocator for the call (which then runs on the current stream)."""
-    import torch
+    L = _load()
+    d = _gpu(logits, "logits")
     T, E = logits.shape
     k, G = topk_ids.shape[-1], counts.shape[0]
     dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
-    args = (logits.data_ptr(), _rows(logits, "logits"), dt, _flat(topk_ids, "topk_ids", T * k, torch.int32),
-            None if valid is None else _flat(valid, "valid", T, (torch.bool, torch.uint8)),
-            _flat(losses, "losses", 2, torch.float32), _flat(counts, "counts", G * E, torch.int32),
-            _flat(tokens, "tokens", G + 1, torch.int32))
+    ld = _rows(logits, "logits", d, T, E)
     if workspace is None:
         if stream is not None:
             raise ValueError("moe_decode_balance on a given stream needs a workspace")
-        workspace = torch.empty(moe_decode_balance_workspace(T, E, k, G), dtype=torch.uint8, device=logits.device)
-    _call("moe_decode_balance", lib().moe_decode_balance, stream,
-          (logits, topk_ids, valid, losses, counts, tokens, workspace), *args,
-          _flat(workspace, "workspace", workspace.numel(), torch.uint8), workspace.numel(), T, E, k, G)
+        workspace = _torch.empty(moe_decode_balance_workspace(T, E, k, G), dtype=_u8, device=logits.device)
+    n = workspace.numel()
+    _call("moe_decode_balance", L.moe_decode_balance, d, stream, logits.data_ptr(), ld, dt,
+          _flat(topk_ids, "topk_ids", d, T * k, _i32), None if valid is None else _flat(valid, "valid", d, T, _flags),
+          _flat(losses, "losses", d, 2, _f32), _flat(counts, "counts", d, G * E, _i32),
+          _flat(tokens, "tokens", d, G + 1, _i32), _flat(workspace, "workspace", d, n, _u8), n, T, E, k, G)
     return losses, counts, tokens
 
 
 def moe_decode_balance_backward(logits, counts, tokens, grad_losses, dlogits, k, valid=None, stream=None):
     """dlogits [T,E] = the gradient of grad_losses . losses of moe_decode_balance with respect to the logits, from
     the counts and tokens that call left (see include/moe_decode.h)."""
-    import torch
+    L = _load()
+    d = _gpu(logits, "logits")
     T, E = logits.shape
     G = counts.shape[0]
     dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
-    if _dtype_code(dlogits, "dlogits", (MOE_F32, MOE_BF16)) != dt:
+    if _codes.get(dlogits.dtype) != dt:
         raise ValueError("dlogits must have the type of logits")
-    _call("moe_decode_balance_backward", lib().moe_decode_balance_backward, stream,
-          (logits, valid, counts, tokens, grad_losses, dlogits),
-          logits.data_ptr(), _rows(logits, "logits"), dt,
-          None if valid is None else _flat(valid, "valid", T, (torch.bool, torch.uint8)),
-          _flat(counts, "counts", G * E, torch.int32), _flat(tokens, "tokens", G + 1, torch.int32),
-          _flat(grad_losses, "grad_losses", 2, torch.float32), dlogits.data_ptr(), _rows(dlogits, "dlogits", T, E),
+    _call("moe_decode_balance_backward", L.moe_decode_balance_backward, d, stream, logits.data_ptr(),
+          _rows(logits, "logits", d, T, E), dt, None if valid is None else _flat(valid, "valid", d, T, _flags),
+          _flat(counts, "counts", d, G * E, _i32), _flat(tokens, "tokens", d, G + 1, _i32),
+          _flat(grad_losses, "grad_losses", d, 2, _f32), dlogits.data_ptr(), _rows(dlogits, "dlogits", d, T, E),
           T, E, k, G)
     return dlogits
 
@@ -412,58 +432,54 @@ def moe_decode_balance_backward(logits, counts, tokens, grad_losses, dlogits, k,
 def moe_decode_quantize_fp8(x, q, scales, swiglu=False, pow2=False, stream=None):
     """q [M,K] E4M3 codes (uint8) and scales fp32 [M, ceil(K/128)] of x [M,K], or with swiglu of
     SiLU(x[:, :K]) * x[:, K:] of x [M,2K]; pow2: scales are powers of two (see include/moe_decode.h)."""
-    import torch
+    L = _load()
+    d = _gpu(x, "x")
     M, K = q.shape
-    dt = _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16))
-    _call("moe_decode_quantize_fp8", lib().moe_decode_quantize_fp8, stream, (x, q, scales),
-          x.data_ptr(), _rows(x, "x", M, 2 * K if swiglu else K), dt, _flat(q, "q", M * K, torch.uint8),
-          _flat(scales, "scales", M * -(-K // 128), torch.float32), M, K,
+    _call("moe_decode_quantize_fp8", L.moe_decode_quantize_fp8, d, stream, x.data_ptr(),
+          _rows(x, "x", d, M, 2 * K if swiglu else K), _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16)),
+          _flat(q, "q", d, M * K, _u8), _flat(scales, "scales", d, M * -(-K // 128), _f32), M, K,
           (MOE_QUANT_SWIGLU if swiglu else 0) | (MOE_QUANT_POW2 if pow2 else 0))
     return q, scales
-
-
-def _codes_rows(x, name, rows=None, cols=None):
-    import torch
-    if x.dtype != torch.uint8:
-        raise ValueError(f"{name} has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
-    return _rows(x, name, rows, cols)
 
 
 def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None):
     """y [M,N] = the product of x [M,K] and w [N,K] (E4M3 codes, uint8) with scales sx [M, ceil(K/128)] and
     sw [ceil(N/128), ceil(K/128)] (see include/moe_decode.h)."""
-    import torch
+    L = _load()
+    d = _gpu(x, "x")
     M, K = x.shape
     N = w.shape[0]
     kb = -(-K // 128)
-    args = (x.data_ptr(), _codes_rows(x, "x"), _flat(sx, "sx", M * kb, torch.float32),
-            _flat(w, "w", N * K, torch.uint8), _flat(sw, "sw", -(-N // 128) * kb, torch.float32),
-            y.data_ptr(), _rows(y, "y", M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), M, N, K)
+    if x.dtype is not _u8:
+        raise ValueError(f"x has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
+    args = (x.data_ptr(), _rows(x, "x", d, M, K), _flat(sx, "sx", d, M * kb, _f32), _flat(w, "w", d, N * K, _u8),
+            _flat(sw, "sw", d, -(-N // 128) * kb, _f32), y.data_ptr(), _rows(y, "y", d, M, N),
+            _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), M, N, K)
     if variant is None:
-        _call("moe_decode_matmul_fp8", lib().moe_decode_matmul_fp8, stream, (x, sx, w, sw, y), *args)
+        _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8, d, stream, *args)
     else:
-        _call("moe_decode_matmul_fp8", lib().moe_decode_matmul_fp8_ex, stream, (x, sx, w, sw, y), *args, int(variant))
+        _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8_ex, d, stream, *args, int(variant))
     return y
 
 
 def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=None, variant=None):
     """The product of moe_decode_matmul_fp8 for E matrices w [E,N,K] on rows sorted by expert, counts [E] (int32) of
     them each; x_rows [M] (int32): the row of x that each row of y comes from (see include/moe_decode.h)."""
-    import torch
+    L = _load()
+    d = _gpu(x, "x")
     X, K = x.shape
-    E, N = w.shape[0], w.shape[1]
-    M = y.shape[0]
+    E, N, M = w.shape[0], w.shape[1], y.shape[0]
     kb = -(-K // 128)
-    args = (x.data_ptr(), _codes_rows(x, "x"), _flat(sx, "sx", X * kb, torch.float32),
-            None if x_rows is None else _flat(x_rows, "x_rows", M, torch.int32),
-            _flat(counts, "counts", E, torch.int32),
-            _flat(w, "w", E * N * K, torch.uint8), _flat(sw, "sw", E * -(-N // 128) * kb, torch.float32),
-            y.data_ptr(), _rows(y, "y", M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), X, M, N, K, E)
-    tensors = (x, sx, x_rows, counts, w, sw, y)
+    if x.dtype is not _u8:
+        raise ValueError(f"x has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
+    args = (x.data_ptr(), _rows(x, "x", d, X, K), _flat(sx, "sx", d, X * kb, _f32),
+            None if x_rows is None else _flat(x_rows, "x_rows", d, M, _i32), _flat(counts, "counts", d, E, _i32),
+            _flat(w, "w", d, E * N * K, _u8), _flat(sw, "sw", d, E * -(-N // 128) * kb, _f32), y.data_ptr(),
+            _rows(y, "y", d, M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), X, M, N, K, E)
     if variant is None:
-        _call("moe_decode_matmul_fp8_experts", lib().moe_decode_matmul_fp8_experts, stream, tensors, *args)
+        _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts, d, stream, *args)
     else:
-        _call("moe_decode_matmul_fp8_experts", lib().moe_decode_matmul_fp8_experts_ex, stream, tensors, *args, int(variant))
+        _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts_ex, d, stream, *args, int(variant))
     return y
 
 

@@ -47,23 +47,114 @@ long long row_tiles(const moe::MatmulArgs& a, int bm) {
 }
 
 template <typename O>
-void go_64(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
-  hipLaunchKernelGGL(moe::matmul_64_kernel<O>, grid, dim3(256), 0, st, a);
+void go_far(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
+  hipLaunchKernelGGL(moe::matmul_far_kernel<O>, grid, dim3(256), 0, st, a);
 }
-long long launch_64(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
-  const long long blocks = row_tiles(a, moe::kMm64) * ((a.N + moe::kMm64 - 1) / moe::kMm64);
+long long launch_far(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+  const long long blocks = row_tiles(a, moe::kMmFar) * ((a.N + moe::kMmFar - 1) / moe::kMmFar);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
-  if (y_dtype == MOE_F32) go_64<float>(grid, st, a);
-  else if (y_dtype == MOE_BF16) go_64<__bf16>(grid, st, a);
-  else go_64<moe::half_t>(grid, st, a);
+  if (y_dtype == MOE_F32) go_far<float>(grid, st, a);
+  else if (y_dtype == MOE_BF16) go_far<__bf16>(grid, st, a);
+  else go_far<moe::half_t>(grid, st, a);
   return blocks;
 }
 
-MatmulLaunch matmul_launcher(int& variant, const moe::MatmulArgs& a) {
-  if (variant == 0) variant = MOE_MATMUL_TILE_64;
+template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
+void go_tile(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
+  hipLaunchKernelGGL((moe::matmul_tile_kernel<BM, BN, WM, WN, S, CP, O>), grid, dim3(64 * WM * WN), 0, st, a);
+}
+template <int BM, int BN, int WM, int WN, int S, int CP = moe::kCached>
+long long launch_tile(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+  const long long blocks = row_tiles(a, BM) * ((a.N + BN - 1) / BN);
+  if (!go) return blocks;
+  const dim3 grid((unsigned)blocks);
+  if (y_dtype == MOE_F32) go_tile<BM, BN, WM, WN, S, CP, float>(grid, st, a);
+  else if (y_dtype == MOE_BF16) go_tile<BM, BN, WM, WN, S, CP, __bf16>(grid, st, a);
+  else go_tile<BM, BN, WM, WN, S, CP, moe::half_t>(grid, st, a);
+  return blocks;
+}
+
+// 16-bit results only: an FP32 one's conversions need more registers than the accumulators leave.
+long long launch_256(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+  const long long blocks = row_tiles(a, 256) * ((a.N + 255) / 256);
+  if (!go) return blocks;
+  const dim3 grid((unsigned)blocks);
+  if (y_dtype == MOE_BF16) go_tile<256, 256, 2, 4, 2, moe::kCached, __bf16>(grid, st, a);
+  else go_tile<256, 256, 2, 4, 2, moe::kCached, moe::half_t>(grid, st, a);
+  return blocks;
+}
+
+template <int NT, int WK, typename O>
+void go_rows(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
+  hipLaunchKernelGGL((moe::matmul_rows_kernel<NT, WK, O>), grid, dim3(64 * WK), 0, st, a);
+}
+template <int NT, int WK>
+long long launch_rows(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+  const long long blocks = row_tiles(a, 16) * ((a.N + 16 * NT - 1) / (16 * NT));
+  if (!go) return blocks;
+  const dim3 grid((unsigned)blocks);
+  if (y_dtype == MOE_F32) go_rows<NT, WK, float>(grid, st, a);
+  else if (y_dtype == MOE_BF16) go_rows<NT, WK, __bf16>(grid, st, a);
+  else go_rows<NT, WK, moe::half_t>(grid, st, a);
+  return blocks;
+}
+
+// The tile kernels' 32-bit offsets reach every row of a tile of bm rows.
+bool tile_allowed(const moe::MatmulArgs& a, int bm) {
+  return (a.x_rows ? (long long)a.X * a.ldx : (bm - 1) * a.ldx + a.K) <= (long long)moe::kMmOutOfRange;
+}
+
+// The built-in choice, from sweeps on MI355X (us; K = 2048 unless stated; the
+// variants that the rule chooses between, its choice first).
+// One matrix: the smallest tiles while larger ones would leave CUs without
+// work, then the largest that still fill the chip.
+//   16 rows: M = 1, N = 4096 4.4, 64 x 64 7.0; M = 32, N = 1536 (192
+//     workgroups) 5.8, 7.0; N = 2048, K = 4096 (256) 8.2, 10.8; but N = 4096
+//     (512) 8.1, 7.1
+//   64 x 64: N = 4096, M = 256 (256 workgroups) 9.0, 64 x 128 10.5; M = 384 (384) 12.7, 10.9
+//   64 x 128: N = 4096, M = 1024 (512) 17.5, 128 x 128 17.5; N = 2048, K = 4096,
+//     M = 1024 17.7, 27.3; N = 4096, M = 1536 (768) 23.5, 21.1
+//   256 x 256: M = N = 4096 (256) 38.4, 128 x 128 41.8; M = 2048 (128) 34.5, 23.1
+// Experts (128 of 1536 x 2048, top-8), by the rows r of an expert on average:
+//   64 x 128 with w as streaming data: r = 2 53.1, cached 60.4; r = 16 70.5,
+//     79.4; r = 32 86.7, 89.5; r = 64 (w is read for a second tile) 124, 106
+//   128 x 128: r = 96 126.1, 64 x 128 126.6; r = 128 140, 149; r = 64 113, 106
+//   256 x 256: r = 187 160, 128 x 128 168; r = 128 150, 140
+//   64 x 64 while 64 x 128 would not fill the chip: M = 8 8.8, 10.1
+// FP32 results (half the matrix rate): 64 x 64 up to 512 workgroups (N = 4096,
+// M = 512 17.3, 64 x 128 17.6, 128 x 128 24.3), then 128 x 128 (M = 4096 71.6, 64 x 128 83.1).
+int default_variant(const moe::MatmulArgs& a, bool f32) {
+  auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  int v;
+  if (a.E) {
+    const long long r = a.M / a.E;
+    const long long few = (long long)(a.M < a.E ? a.M : a.E) * ((a.N + 127) / 128);
+    v = few <= 256 ? MOE_MATMUL_TILE_64X64
+        : r <= 32 ? MOE_MATMUL_TILE_64X128_STREAM
+        : r <= 95 ? MOE_MATMUL_TILE_64X128
+        : r <= 159 || f32 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
+  } else {
+    v = a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16
+        : tiles(64, 64) <= (f32 ? 512 : 256) ? MOE_MATMUL_TILE_64X64
+        : !f32 && tiles(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+        : f32 || tiles(256, 256) < 192 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
+  }
+  const int bm = v == MOE_MATMUL_TILE_256X256 ? 256 : v == MOE_MATMUL_TILE_128X128 ? 128 : 64;
+  return v == MOE_MATMUL_ROWS_16 || tile_allowed(a, bm) ? v : MOE_MATMUL_FAR_ROWS;
+}
+
+MatmulLaunch matmul_launcher(int& variant, const moe::MatmulArgs& a, int y_dtype) {
+  if (variant == 0) variant = default_variant(a, y_dtype == MOE_F32);
   switch (variant) {
-    case MOE_MATMUL_TILE_64: return launch_64;
+    // 8 wavefronts along K where each of 4 would take more than 4 turns: K = 4096, M = 1 5.9 against 6.7 us; K = 2048 4.6 against 4.4
+    case MOE_MATMUL_ROWS_16: return a.kb > 16 ? launch_rows<1, 8> : launch_rows<1, 4>;
+    case MOE_MATMUL_TILE_64X64: return tile_allowed(a, 64) ? launch_tile<64, 64, 2, 2, 3> : nullptr;
+    case MOE_MATMUL_TILE_64X128: return tile_allowed(a, 64) ? launch_tile<64, 128, 2, 2, 3> : nullptr;
+    case MOE_MATMUL_TILE_64X128_STREAM: return tile_allowed(a, 64) ? launch_tile<64, 128, 2, 2, 3, moe::kStream> : nullptr;
+    case MOE_MATMUL_TILE_128X128: return tile_allowed(a, 128) ? launch_tile<128, 128, 2, 2, 2> : nullptr;
+    case MOE_MATMUL_TILE_256X256: return tile_allowed(a, 256) && y_dtype != MOE_F32 ? launch_256 : nullptr;
+    case MOE_MATMUL_FAR_ROWS: return launch_far;
   }
   return nullptr;
 }
@@ -85,7 +176,7 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
   if (X == 0 || (!x_rows && X < M) || !stride_ok(X, K, ldx) || !stride_ok(M, N, ldy)) return MOE_ERR_SHAPE;
   if (X == 1) ldx = K;   // never used
   if (M == 1) ldy = N;
-  if (ldx % 16 || (x_rows && (long long)X * ldx >= (1LL << 32))) return MOE_ERR_SHAPE;
+  if (ldx % 16) return MOE_ERR_SHAPE;
   if (!x || !sx || !w || !sw || !y || (experts && !counts)) return MOE_ERR_NULL;
   const size_t os = dtype_size(y_dtype);
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(y, os) ||
@@ -99,7 +190,7 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
                         experts ? (size_t)E * 4 : 0, mats * N * K, mats * a.nb * a.kb * 4};
   for (int i = 0; i < 6; ++i)
     if (overlaps(y, row_bytes(M, N, ldy, os), in[i], inb[i])) return MOE_ERR_ALIAS;
-  MatmulLaunch fn = matmul_launcher(variant, a);
+  MatmulLaunch fn = matmul_launcher(variant, a, y_dtype);
   if (!fn) return MOE_ERR_ARG;
   if (fn(false, nullptr, a, y_dtype) >= (1LL << 22)) return MOE_ERR_SHAPE;   // a launch holds fewer than 2^32 threads
   (void)hipGetLastError();
@@ -165,7 +256,7 @@ int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int* variant, int* wo
   moe::MatmulArgs a{};
   a.X = M, a.M = M, a.N = N, a.K = K, a.E = E, a.kb = (K + 127) / 128, a.nb = (N + 127) / 128;
   int v = 0;
-  MatmulLaunch fn = matmul_launcher(v, a);
+  MatmulLaunch fn = matmul_launcher(v, a, MOE_BF16);
   *variant = v;
   *workgroups = (int)fn(false, nullptr, a, MOE_BF16);
   return MOE_OK;

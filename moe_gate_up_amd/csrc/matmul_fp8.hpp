@@ -50,36 +50,83 @@ struct MatmulArgs {
   bool wide;                   // y's rows take 4-element stores
 };
 
-// The rows of y that m-tile t of BM rows covers, and their expert.
-struct RowTile {
-  int expert, first, rows;   // rows == 0: there is no such tile
+// The tile of y that a workgroup computes: rows [first, first + rows) and
+// column tile nt, by the matrix of `expert`.  rows == 0: nothing to do.
+struct MmTile {
+  int expert, first, rows, nt;
 };
 
-// With experts, every expert's rows are cut into tiles of their own.  One
-// wavefront looks at 64 experts at a time: a prefix sum over the lanes gives
-// each expert's first tile and first row.
+// One matrix: blocks of 8 tiles of rows, a column of 8 after the other, so that
+// the 32 workgroups at work on an XCD (which has one range of the tiles) share
+// 8 tiles of x and 4 of w.
 template <int BM>
-__device__ __forceinline__ RowTile find_rows(const MatmulArgs& a, int t, int lane) {
-  if (!a.counts) return {0, t * BM, min(BM, a.M - t * BM)};
+__device__ __forceinline__ MmTile tile_of_matrix(const MatmulArgs& a, int n_tiles) {
+  const int id = xcd_contiguous_block((int)blockIdx.x, (int)gridDim.x);
+  const int m_tiles = (int)gridDim.x / n_tiles, group = id / (8 * n_tiles);
+  const int gm = min(8, m_tiles - 8 * group), r = id - 8 * group * n_tiles;
+  const int nt = r / gm, mt = 8 * group + r - nt * gm;
+  return {0, mt * BM, min(BM, a.M - mt * BM), nt};
+}
+
+// Experts: each one's rows are cut into tiles of their own, all columns of one
+// tile of rows after the other.  How many tiles that makes is known on the
+// device only, and the grid is what it can be at most; the XCDs share out the
+// tiles that there are (by the grid, the last of them would have none: 128
+// experts of 1536 x 2048 and 32768 rows, 238 against 204 us).  A wavefront looks at 64 experts at
+// a time (the counts of 256 requested at once): a prefix sum over the lanes
+// gives each expert's first tile and first row.
+template <int BM>
+__device__ __forceinline__ MmTile tile_of_experts(const MatmulArgs& a, int n_tiles, int lane) {
+  int c4[4];
+  auto request = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c4[i] = a.counts[min(e0 + 64 * i + lane, a.E - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c4[i] = e0 + 64 * i + lane < a.E ? min(max(c4[i], 0), a.M) : 0;
+  };
+  // rows and tiles of the experts before the current 64
   int tiles0 = 0, rows0 = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    const int e = e0 + lane;
-    const int c = e < a.E ? min(max(a.counts[e], 0), a.M) : 0;
-    const int r1 = rows0 + wave_incl_scan(c), r0 = r1 - c;
-    const int used = min(r1, a.M) - min(r0, a.M);        // rows beyond M are not computed
-    const int n = (used + BM - 1) / BM;
-    const int t1 = tiles0 + wave_incl_scan(n);
-    const uint64_t hit = __builtin_amdgcn_ballot_w64(t < t1);
-    if (hit) {
-      const int at = (int)__builtin_ctzll(hit);
-      const int i = t - (__builtin_amdgcn_readlane(t1, at) - __builtin_amdgcn_readlane(n, at));
-      const int first = __builtin_amdgcn_readlane(r0, at) + i * BM;
-      return {e0 + at, first, min(BM, __builtin_amdgcn_readlane(used, at) - i * BM)};
-    }
+  // this lane's expert: its first row, its rows (those beyond M are not computed), the tiles up to its end
+  auto scan = [&](int c, int& r0, int& used, int& n, int& t1) {
+    const int r1 = rows0 + wave_incl_scan(c);
+    r0 = r1 - c;
+    used = min(r1, a.M) - min(r0, a.M);
+    n = (used + BM - 1) / BM;
+    t1 = tiles0 + wave_incl_scan(n);
     tiles0 = __builtin_amdgcn_readlane(t1, 63);
     rows0 = min(__builtin_amdgcn_readlane(r1, 63), a.M);
+  };
+  int r0, used, n, t1;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    request(e0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scan(c4[i], r0, used, n, t1);
   }
-  return {0, 0, 0};
+  const int total = tiles0 * n_tiles;
+  if ((int)blockIdx.x >= total) return {0, 0, 0, 0};
+  const int id = xcd_contiguous_block((int)blockIdx.x, total);
+  const int mt = id / n_tiles;
+  tiles0 = rows0 = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    if (a.E > 256) request(e0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      scan(c4[i], r0, used, n, t1);
+      const uint64_t hit = __builtin_amdgcn_ballot_w64(mt < t1);
+      if (hit) {
+        const int at = (int)__builtin_ctzll(hit);
+        const int k = mt - (__builtin_amdgcn_readlane(t1, at) - __builtin_amdgcn_readlane(n, at));
+        const int rows = __builtin_amdgcn_readlane(used, at) - k * BM;
+        return {e0 + 64 * i + at, __builtin_amdgcn_readlane(r0, at) + k * BM, min(BM, rows), id - mt * n_tiles};
+      }
+    }
+  }
+  return {0, 0, 0, 0};
+}
+
+template <int BM>
+__device__ __forceinline__ MmTile tile_of(const MatmulArgs& a, int n_tiles, int lane) {
+  return a.counts ? tile_of_experts<BM>(a, n_tiles, lane) : tile_of_matrix<BM>(a, n_tiles);
 }
 
 // 8 E4M3 codes -> 8 bf16 (exact).
@@ -121,21 +168,21 @@ __device__ __forceinline__ void store4(O* p, const f32x4& v, int left, bool wide
   }
 }
 
-// A 64 x 64 tile of y per workgroup, 4 wavefronts of 32 x 32.  The 64 rows of
-// each operand are staged through registers into LDS, one block of K at a
+// The kernel for rows of x further apart than 32-bit offsets reach, and the
+// simplest one: a 64 x 64 tile of y per workgroup, 4 wavefronts of 32 x 32.  The
+// 64 rows of each operand are staged through registers into LDS, one block of K at a
 // time; piece p of row r lies at position p ^ (r % 8), so that the 16 rows of
 // one operand read fall into different banks.
-constexpr int kMm64 = 64;
+constexpr int kMmFar = 64;
 template <typename O>
-__global__ __launch_bounds__(256) void matmul_64_kernel(MatmulArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kMm64 * kMmBlock];
+__global__ __launch_bounds__(256) void matmul_far_kernel(MatmulArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kMmFar * kMmBlock];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
-  const int n_tiles = (a.N + kMm64 - 1) / kMm64;
-  const int mt = (int)blockIdx.x / n_tiles, nt = (int)blockIdx.x - mt * n_tiles;
-  const RowTile rt = find_rows<kMm64>(a, mt, lane);
+  const int n_tiles = (a.N + kMmFar - 1) / kMmFar;
+  const MmTile rt = tile_of<kMmFar>(a, n_tiles, lane);
   if (rt.rows <= 0) return;
-  const int n0 = nt * kMm64;
+  const int n0 = rt.nt * kMmFar;
   const uint8_t* wm = a.w + (size_t)rt.expert * a.N * a.K;
   const float* sw = a.sw + ((size_t)rt.expert * a.nb + n0 / kMmBlock) * a.kb;
 
@@ -223,6 +270,345 @@ __global__ __launch_bounds__(256) void matmul_64_kernel(MatmulArgs a) {
       if (bad[j]) v = f32x4{qnan(), qnan(), qnan(), qnan()};
       store4(row + n, v, a.N - n, a.wide);
     }
+  }
+}
+
+template <int V>
+struct MmInt {
+  static constexpr int value = V;
+};
+
+// A buffer offset past every buffer's end: a load from there gives 0.
+constexpr uint32_t kMmOutOfRange = 0xFFFFFFF0u;
+
+// Copies straight into LDS: lane l's SIZE bytes go to lds + SIZE l.
+template <int CP = kCached>
+__device__ __forceinline__ void copy16_to_lds(rsrc_t r, void* lds, uint32_t voff, uint32_t soff) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, CP);
+}
+__device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff, uint32_t soff) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
+}
+
+// A wavefront's MT x NT tiles to y: rows m0 .. of the row tile, columns n0 ..
+// (`inside`: all of the workgroup's columns exist).  A row number outside x
+// makes its row NaN.
+template <typename O, int MT, int NT>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0,
+                                           bool inside, int m0, int lane) {
+  const bool whole = a.wide && inside;
+  const int n = n0 + 4 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int r = m0 + 16 * j + (lane & 15);
+    if (r >= rt.rows) continue;
+    const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
+    const float nan = bad ? qnan() : 0.0f;   // v + 0 is v, but for a -0
+    O* row = static_cast<O*>(a.y) + (long long)(rt.first + r) * a.ldy + n;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
+      if (whole) store4(row + 16 * i, v, 4, true);
+      else store4(row + 16 * i, v, a.N - n - 16 * i, a.wide);
+    }
+  }
+}
+
+// Tiles of BM x BN, WM x WN wavefronts of (BM / WM) x (BN / WN), S buffers: the
+// kernel of prompts.  A block of K of both operands is copied straight from
+// memory into LDS (buffer_load ... lds, 16 bytes a lane) S - 1 blocks ahead of
+// the one that is multiplied.  A copy puts lane l's 16 bytes at the 16 l-th
+// byte of its kilobyte, so the swizzle of the pieces (piece p of row r at
+// p ^ (r % 8)) is made by the lane's choice of what it reads.  Every buffer is
+// an array of its own, so that the compiler can tell a read of one from the
+// copies into the others and does not wait for those.
+//
+// The rows' scales of the block are copied to LDS with it.  The columns' scales
+// are one number a block and wavefront (its columns lie in one block of 128):
+// lane l holds that of block l of the current span.
+template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
+__global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs a) {
+  constexpr int kWaves = WM * WN;
+  constexpr int MT = BM / WM / 16, NT = BN / WN / 16;          // 16 x 16 tiles of one wavefront
+  constexpr int XC = BM / 8 / kWaves, WC = BN / 8 / kWaves;    // copies (8 rows each) of one wavefront
+  constexpr int kOps = XC + WC + 1;                            // copies of one block, with the scales
+  static_assert(BN / WN <= kMmBlock && kMmBlock % (BN / WN) == 0 && XC * 8 * kWaves == BM && WC * 8 * kWaves == BN);
+  static_assert(BM % 64 == 0 && kWaves % (BM / 64) == 0 && S >= 2 && S <= 4 && (S - 2) * kOps < 64);
+  __shared__ __attribute__((aligned(1024))) uint8_t xl0[BM * kMmBlock], xl1[BM * kMmBlock], xl2[(S > 2 ? BM : 1) * kMmBlock],
+      xl3[(S > 3 ? BM : 1) * kMmBlock];
+  __shared__ __attribute__((aligned(1024))) uint8_t wl0[BN * kMmBlock], wl1[BN * kMmBlock], wl2[(S > 2 ? BN : 1) * kMmBlock],
+      wl3[(S > 3 ? BN : 1) * kMmBlock];
+  __shared__ __attribute__((aligned(256))) float sl0[BM], sl1[BM], sl2[S > 2 ? BM : 1], sl3[S > 3 ? BM : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int n_tiles = (a.N + BN - 1) / BN;
+  const MmTile rt = tile_of<BM>(a, n_tiles, lane);
+  if (rt.rows <= 0) return;
+  const int n0 = rt.nt * BN;
+  // wavefronts w and w + 4 share a SIMD: they differ in their rows, so that a tile of few rows leaves half of every
+  // SIMD's work undone rather than all of half of them
+  const int wm = w / WN * (BM / WM), wn = w % WN * (BN / WN);
+  const bool idle = wm >= rt.rows;   // copies and barriers only
+
+  // with row numbers the buffers start at x, else at the tile's first row
+  const uint8_t* xb = a.x_rows ? a.x : a.x + (long long)rt.first * a.ldx;
+  const float* sb = a.x_rows ? a.sx : a.sx + (long long)rt.first * a.kb;
+  const rsrc_t xr = make_rsrc(xb, kMmOutOfRange), sr = make_rsrc(sb, kMmOutOfRange);
+  const rsrc_t wr = make_rsrc(a.w + (size_t)rt.expert * a.N * a.K, (uint64_t)a.N * a.K);
+  const rsrc_t swr = make_rsrc(a.sw + (size_t)rt.expert * a.nb * a.kb, (uint64_t)a.nb * a.kb * 4);
+  const int piece = (lane & 7) ^ (lane >> 3);   // of the 8 pieces of this lane's row in each copy
+  int row[XC + 1];   // rows behind xb: this lane's of each copy, and of the scales; past the tile its last row again
+#pragma unroll
+  for (int j = 0; j < XC; ++j) row[j] = min((w * XC + j) * 8 + (lane >> 3), rt.rows - 1);
+  row[XC] = min(w % (BM / 64) * 64 + lane, rt.rows - 1);
+  if (a.x_rows) {
+#pragma unroll
+    for (int j = 0; j <= XC; ++j) row[j] = a.x_rows[rt.first + row[j]];
+#pragma unroll
+    for (int j = 0; j <= XC; ++j) row[j] = (unsigned)row[j] < (unsigned)a.X ? row[j] : 0;
+  }
+  uint32_t xo[XC], wo[WC], so = (uint32_t)row[XC] * (uint32_t)a.kb * 4u;
+#pragma unroll
+  for (int j = 0; j < XC; ++j) {
+    xo[j] = (uint32_t)row[j] * (uint32_t)a.ldx + 16u * piece;
+    asm("" : "+v"(xo[j]));   // 32 bits, and no more than that, live through the loop
+  }
+#pragma unroll
+  for (int j = 0; j < WC; ++j) {
+    wo[j] = (uint32_t)min(n0 + (w * WC + j) * 8 + (lane >> 3), a.N - 1) * (uint32_t)a.K + 16u * piece;
+    asm("" : "+v"(wo[j]));
+  }
+  const uint32_t swo = (uint32_t)min((n0 + wn) / kMmBlock, a.nb - 1) * (uint32_t)a.kb * 4u + 4u * lane;
+  float sw64 = 0.0f;   // lane l: the columns' scale of block sw_first + l
+  int sw_first = 0;
+  auto copy = [&](uint8_t* xl, uint8_t* wl, float* sl, int b) {
+    const uint32_t k = (uint32_t)b * kMmBlock;
+    if ((int)k + kMmBlock > a.K) {   // K ends in or before the block: zeros behind K, read out of range
+      const bool in = (int)k + 16 * piece < a.K;
+#pragma unroll
+      for (int j = 0; j < XC; ++j) xo[j] = in ? xo[j] : kMmOutOfRange;
+#pragma unroll
+      for (int j = 0; j < WC; ++j) wo[j] = in ? wo[j] : kMmOutOfRange;
+      so = b < a.kb ? so : kMmOutOfRange;
+    }
+#pragma unroll
+    for (int j = 0; j < XC; ++j) copy16_to_lds(xr, xl + (w * XC + j) * 1024, xo[j], k);
+#pragma unroll
+    for (int j = 0; j < WC; ++j) copy16_to_lds<CP>(wr, wl + (w * WC + j) * 1024, wo[j], k);
+    copy4_to_lds(sr, sl + w % (BM / 64) * 64, so, 4u * b);
+  };
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  // where this lane's pieces of its wavefront's first tile lie
+  const uint32_t x0 = (wm + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), x1 = x0 ^ 64;
+  const uint32_t w0 = (wn + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), w1 = w0 ^ 64;
+  auto operand = [&](const uint8_t* base, uint32_t o0, uint32_t o1) {
+    const u32x4 u = *reinterpret_cast<const u32x4*>(base + o0);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(base + o1);
+    return i32x8_t{(int)u.v[0], (int)u.v[1], (int)u.v[2], (int)u.v[3], (int)v.v[0], (int)v.v[1], (int)v.v[2], (int)v.v[3]};
+  };
+  // One block, product by product: while one is formed, the one kLag before it
+  // is scaled and added (the last ones of a block at the next block's first),
+  // so that the vector unit never waits for a product nor the matrix unit for
+  // it.  The barriers to the scheduler keep that order: left alone it asks for
+  // more registers than there are.
+  constexpr int kLag = NT >= 4 ? 3 : 1, kRing = kLag + 1, kTiles = MT * NT;   // a lag within one row tile and the one before
+  static_assert(kTiles % kRing == 0, "a block begins at the ring's first slot");
+  f32x4 p[kRing];
+  float s_prev = 0.0f;   // the scale of the block's last row tile, for the products that wait
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) p[i] = f32x4{0, 0, 0, 0};
+  auto add = [&](int t, int slot, float s) {
+    f32x4& o = acc[t % NT][t / NT];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(p[slot][c], s, o[c]);
+    asm volatile("" : "+v"(o));   // here, and not sunk behind the products that follow
+  };
+  auto scales = [&] {   // past the last block: never used
+    sw64 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(swr, swo + 4u * sw_first, 0, 0));
+  };
+  auto multiply = [&](const uint8_t* xl, const uint8_t* wl, const float* sl, int b) {
+    if (idle) return;
+    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw64), b - sw_first));
+    i32x8_t f[NT], x[2];
+    float s[2], raw = 0.0f;
+    f[0] = operand(wl, w0, w1);
+    x[0] = operand(xl, x0, x1);
+    s[0] = sl[wm + lr] * sw;
+#pragma unroll
+    for (int i = 1; i < NT; ++i) f[i] = operand(wl + 16 * kMmBlock * i, w0, w1);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int j = t / NT, i = t % NT;
+      if (i == 0 && j + 1 < MT) {
+        x[(j + 1) & 1] = operand(xl + 16 * kMmBlock * (j + 1), x0, x1);
+        raw = sl[wm + 16 * (j + 1) + lr];
+      }
+      const f32x4 q = block_product<sizeof(O) == 4>(f[i], x[j & 1]);
+      const int u = t - kLag;
+      add((u + kTiles) % kTiles, (u < 0 ? u + kTiles : u) % kRing, u < 0 ? s_prev : s[(u / NT) & 1]);
+      p[t % kRing] = q;
+      if (i == NT - 1 && j + 1 < MT) s[(j + 1) & 1] = raw * sw;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    s_prev = s[(MT - 1) & 1];
+  };
+  // everyone's copies of the block have arrived (later ones may be on their way),
+  // and everyone is done with the buffer that the next copies fill
+  auto turn = [&](auto later) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(decltype(later)::value * kOps) & ~0x0F00);   // and lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  constexpr MmInt<S - 2> kLater{};
+  constexpr MmInt<0> kNone{};
+
+  scales();   // older than the copies: there when the first block's are
+  copy(xl0, wl0, sl0, 0);
+  if constexpr (S > 2) copy(xl1, wl1, sl1, 1);
+  if constexpr (S > 3) copy(xl2, wl2, sl2, 2);
+  int b = 0;
+  constexpr int kSpan = 60;   // blocks whose columns' scales are held at a time: whole rounds of the buffers
+  for (;;) {
+    for (; b + S <= min(a.kb, sw_first + kSpan); b += S) {
+      turn(kLater);
+      if constexpr (S == 2) copy(xl1, wl1, sl1, b + 1);
+      else if constexpr (S == 3) copy(xl2, wl2, sl2, b + 2);
+      else copy(xl3, wl3, sl3, b + 3);
+      multiply(xl0, wl0, sl0, b);
+      turn(kLater);
+      copy(xl0, wl0, sl0, b + S);
+      multiply(xl1, wl1, sl1, b + 1);
+      if constexpr (S > 2) {
+        turn(kLater);
+        copy(xl1, wl1, sl1, b + S + 1);
+        multiply(xl2, wl2, sl2, b + 2);
+      }
+      if constexpr (S > 3) {
+        turn(kLater);
+        copy(xl2, wl2, sl2, b + S + 2);
+        multiply(xl3, wl3, sl3, b + 3);
+      }
+    }
+    if (sw_first + kSpan >= a.kb) break;
+    sw_first += kSpan;
+    scales();
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  }
+  turn(kNone);   // no copy outlives the loop
+  if (b < a.kb) multiply(xl0, wl0, sl0, b);
+  if constexpr (S > 2)
+    if (b + 1 < a.kb) multiply(xl1, wl1, sl1, b + 1);
+  if constexpr (S > 3)
+    if (b + 2 < a.kb) multiply(xl2, wl2, sl2, b + 2);
+#pragma unroll
+  for (int u = 0; u < kLag; ++u) add(kTiles - kLag + u, (kTiles - kLag + u) % kRing, s_prev);
+
+  store_tile<O, MT, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane);
+}
+
+// Tiles of 16 rows: the kernel of decode, where a matrix is read for a handful
+// of rows and its bytes are all that counts.  16 NT columns a workgroup; its WK
+// wavefronts take turns along K, 4 blocks (512 bytes of each row of w) at a
+// time, all loads of the next turn requested before this one's products are
+// formed, straight into the registers that the products take them from.  The
+// wavefronts' sums are added in LDS, in their order.  w is read once, as
+// streaming data; the products are the exact ones for every type of y: the
+// matrix cores wait for memory all the same.
+template <int NT, int WK, typename O>
+__global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
+  constexpr int BN = 16 * NT, kTurn = 4;
+  static_assert(kMmBlock % BN == 0 && NT <= WK);
+  __shared__ f32x4 part[WK][NT][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int n_tiles = (a.N + BN - 1) / BN;
+  const MmTile rt = tile_of<16>(a, n_tiles, lane);
+  if (rt.rows <= 0) return;
+  const int n0 = rt.nt * BN;
+
+  const int m = rt.first + min(lr, rt.rows - 1);
+  const int xr = a.x_rows ? a.x_rows[m] : m;
+  const bool bad = (unsigned)xr >= (unsigned)a.X;
+  const uint8_t* x = a.x + (long long)(bad ? 0 : xr) * a.ldx + 16 * lq;
+  const float* sx = a.sx + (long long)(bad ? 0 : xr) * a.kb;
+  const float* sw = a.sw + ((size_t)rt.expert * a.nb + n0 / kMmBlock) * a.kb;
+  const rsrc_t wr = make_rsrc(a.w + (size_t)rt.expert * a.N * a.K, (uint64_t)a.N * a.K);
+  uint32_t wo[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) wo[i] = (uint32_t)min(n0 + 16 * i + lr, a.N - 1) * (uint32_t)a.K + 16u * lq;
+
+  struct Turn {
+    u32x4 f[kTurn][NT][2], x[kTurn][2];
+    float s[kTurn];
+  };
+  // blocks b .. b + 3; pieces behind K are zeros
+  auto load = [&](Turn& t, int b) {
+#pragma unroll
+    for (int c = 0; c < kTurn; ++c) {
+      const int k = (b + c) * kMmBlock;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 64 * h + 16 * lq < a.K;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          t.f[c][i][h] = bload16<kStream>(wr, in ? wo[i] + (uint32_t)(k + 64 * h) : kMmOutOfRange, 0);
+        t.x[c][h] = u32x4{{0, 0, 0, 0}};
+        if (in) t.x[c][h] = *reinterpret_cast<const u32x4*>(x + k + 64 * h);
+      }
+      const int bc = min(b + c, a.kb - 1);
+      t.s[c] = sx[bc] * sw[bc];
+    }
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+  auto join = [](const u32x4& u, const u32x4& v) {
+    return i32x8_t{(int)u.v[0], (int)u.v[1], (int)u.v[2], (int)u.v[3], (int)v.v[0], (int)v.v[1], (int)v.v[2], (int)v.v[3]};
+  };
+  auto multiply = [&](const Turn& t, int b) {
+#pragma unroll
+    for (int c = 0; c < kTurn; ++c) {
+      const float s = b + c < a.kb ? t.s[c] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const f32x4 p = block_product<true>(join(t.f[c][i][0], t.f[c][i][1]), join(t.x[c][0], t.x[c][1]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(p[j], s, acc[i][j]);
+      }
+    }
+  };
+  Turn t0, t1;
+  int b = kTurn * w;
+  load(t0, b);
+  for (; b < a.kb; b += 2 * kTurn * WK) {
+    const int b1 = b + kTurn * WK;
+    if (b1 < a.kb) load(t1, b1);
+    multiply(t0, b);
+    if (b1 >= a.kb) break;
+    if (b1 + kTurn * WK < a.kb) load(t0, b1 + kTurn * WK);
+    multiply(t1, b1);
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) part[w][i][lane] = acc[i];
+  __syncthreads();
+  if (w >= NT) return;
+  f32x4 v = part[0][w][lane];
+#pragma unroll
+  for (int k = 1; k < WK; ++k) v += part[k][w][lane];
+  if (bad) v = f32x4{qnan(), qnan(), qnan(), qnan()};
+  if (lr < rt.rows) {
+    const int n = n0 + 16 * w + 4 * lq;
+    store4(static_cast<O*>(a.y) + (long long)(rt.first + lr) * a.ldy + n, v, a.N - n, a.wide);
   }
 }
 

@@ -140,9 +140,17 @@ def test_experts_refusals():
     assert experts(rows=at(8, 2)) == mg.MOE_ERR_ALIGN
     assert experts(y=at(5)) == mg.MOE_ERR_ALIAS
     assert experts(y=at(6)) == mg.MOE_ERR_ALIAS
-    for bad in (dict(E=0), dict(E=1025), dict(M=1 << 24), dict(X=-1), dict(X=0), dict(rows=0, X=255),
-                dict(X=1 << 21)):   # 2^21 rows of 2048 bytes to pick from: offsets pass 32 bits
+    for bad in (dict(E=0), dict(E=1025), dict(M=1 << 24), dict(X=-1), dict(X=0), dict(rows=0, X=255)):
         assert experts(**bad) == mg.MOE_ERR_SHAPE, bad
+
+
+def test_variants_refuse_what_they_cannot_reach():
+    far = dict(ldx=1 << 29)                        # 128 such rows pass 32-bit offsets
+    for v in (mg.MOE_MATMUL_TILE_64X64, mg.MOE_MATMUL_TILE_64X128, mg.MOE_MATMUL_TILE_64X128_STREAM,
+              mg.MOE_MATMUL_TILE_128X128, mg.MOE_MATMUL_TILE_256X256):
+        assert matmul(variant=v, M=300, **far) == mg.MOE_ERR_ARG
+        assert experts(variant=v, X=1 << 21) == mg.MOE_ERR_ARG      # 2^21 rows of 2048 bytes to pick from
+    assert matmul(variant=mg.MOE_MATMUL_TILE_256X256, dtype=mg.MOE_F32) == mg.MOE_ERR_ARG
 
 
 def test_plan_names_a_variant():

@@ -74,6 +74,11 @@ def check(y, ref, size, K, what):
     assert rel <= (1e-6 if eps < 1e-6 else eps / 2 + 1e-4), (what, rel)
 
 
+def refused(out, variant):
+    """The largest tile has no form for FP32 results."""
+    return out == "f32" and variant == mg.MOE_MATMUL_TILE_256X256
+
+
 def dense(dev, M, N, K, out, variant, seed=0, pad_x=0, pad_y=0, off_y=0):
     x, sx, w, sw = make(seed + M + N + K, M, N, K)
     X, W = values(x, sx, False), values(w, sw, True)
@@ -82,6 +87,10 @@ def dense(dev, M, N, K, out, variant, seed=0, pad_x=0, pad_y=0, off_y=0):
     xd[:, :K] = x.to(dev)
     yd = torch.full((M, N + pad_y + off_y), 5.0, dtype=TYPES[out], device=dev)
     y = yd[:, off_y:off_y + N]
+    if refused(out, variant):
+        with pytest.raises(mg.MoeDecodeError):
+            mg.moe_decode_matmul_fp8(xd[:, :K], sx.to(dev), w.to(dev), sw.to(dev), y, variant=variant)
+        return
     mg.moe_decode_matmul_fp8(xd[:, :K], sx.to(dev), w.to(dev), sw.to(dev), y, variant=variant or None)
     torch.cuda.synchronize()
     check(y, ref, size, K, f"M={M} N={N} K={K} {out} variant {variant} pads {pad_x} {pad_y} {off_y}")
@@ -92,6 +101,7 @@ SHAPES = [
     (1, 1, 16), (1, 128, 128), (1, 4096, 2048), (2, 64, 144), (5, 100, 2064), (16, 512, 4096), (17, 130, 512), (31, 257, 1040),
     (33, 96, 272), (63, 65, 64), (64, 64, 128), (65, 127, 256), (100, 300, 400), (128, 128, 1536), (129, 256, 768), (200, 1003, 1040),
     (256, 256, 128), (257, 513, 384), (300, 40, 2048), (513, 259, 640), (777, 384, 48),
+    (40, 70, 8336), (130, 140, 16528), (257, 130, 24576),   # more than 64 blocks along K
 ]
 
 
@@ -167,6 +177,11 @@ def grouped(dev, tokens, E, k, N, K, out, variant, gather=True, skew=0.0, extra=
         pad = torch.full((extra, K), 0x7F, dtype=torch.uint8)
         xd, sxd = torch.cat([x[rows.long()], pad]).to(dev), torch.cat([sx[rows.long()], torch.ones(extra, sx.shape[1])]).to(dev)
     y = torch.full((M, N), 5.0, dtype=TYPES[out], device=dev)
+    if refused(out, variant):
+        with pytest.raises(mg.MoeDecodeError):
+            mg.moe_decode_matmul_fp8_experts(xd, sxd, counts.to(dev), w.to(dev), sw.to(dev), y, variant=variant,
+                                             x_rows=rows_d if gather else None)
+        return
     mg.moe_decode_matmul_fp8_experts(xd, sxd, counts.to(dev), w.to(dev), sw.to(dev), y, x_rows=rows_d if gather else None,
                                      variant=variant or None)
     torch.cuda.synchronize()
@@ -202,7 +217,8 @@ def test_experts_odd_counts(dev, variant):
     rows[10], rows[77], rows[120] = -1, 40, 2 ** 31 - 1
     for counts, ends in (([0] * 9, []), ([-3, 20, 0, 70, -2147483648, 1, 0, 30, 0], [0, 20, 20, 90, 90, 91, 91, 121, 121]),
                          ([100, 0, 2147483647, 5, 5, 5, 5, 5, 5], [100, 100, 150]), ([0] * 8 + [1], [0] * 8 + [1])):
-        y = torch.full((M, N), 5.0, dtype=torch.float32, device=dev)
+        out = torch.bfloat16 if refused("f32", variant) else torch.float32
+        y = torch.full((M, N), 5.0, dtype=out, device=dev)
         mg.moe_decode_matmul_fp8_experts(x.to(dev), sx.to(dev), torch.tensor(counts, dtype=torch.int32, device=dev), w.to(dev),
                                          sw.to(dev), y, x_rows=rows.to(dev), variant=variant or None)
         torch.cuda.synchronize()
@@ -212,7 +228,10 @@ def test_experts_odd_counts(dev, variant):
                 r = int(rows[m])
                 if 0 <= r < 40:
                     ref, size = X[r] @ W[e].t(), X[r].abs() @ W[e].abs().t()
-                    assert torch.all((y[m].double() - ref).abs() <= (K + 8) * 2.0 ** -24 * size + 1e-30), (counts, m)
+                    tol = (K + 8) * 2.0 ** -24 * size + 1e-30
+                    if out == torch.bfloat16:
+                        tol = tol + 7 / 8 * 2.0 ** -10 * size + 2.0 ** -8 * ref.abs() * (1 + 2.0 ** -8)
+                    assert torch.all((y[m].double() - ref).abs() <= tol), (counts, m)
                 else:
                     assert torch.isnan(y[m]).all(), (counts, m)
             done = end
@@ -261,9 +280,32 @@ def test_rows_beyond_32_bit_offsets(dev):
     X, W = values(x, sx, False), values(w, sw, True)
     for variant in VARIANTS:
         yd.zero_()
-        mg.moe_decode_matmul_fp8(xd, sx.to(dev), w.to(dev), sw.to(dev), yd, variant=variant or None)
+        try:
+            mg.moe_decode_matmul_fp8(xd, sx.to(dev), w.to(dev), sw.to(dev), yd, variant=variant or None)
+        except mg.MoeDecodeError as e:   # a variant whose 32-bit offsets do not reach a tile's rows refuses the call
+            assert variant and e.code == mg.MOE_ERR_ARG
+            continue
         torch.cuda.synchronize()
         check(yd.contiguous(), X @ W.t(), X.abs() @ W.abs().t(), K, f"far rows variant {variant}")
+
+
+def test_experts_rows_beyond_32_bit_offsets(dev):
+    """Rows picked from a tensor of more than 2^32 bytes."""
+    tokens, E, k, N, K, ld = 9, 3, 2, 200, 272, 1 << 29
+    g = torch.Generator().manual_seed(3)
+    rows, counts, expert = route(g, tokens, E, k, 0.0)
+    x, sx, w, sw = make(8, tokens, N, K, E)
+    xd = torch.empty((tokens - 1) * ld + K, dtype=torch.uint8, device=dev).as_strided((tokens, K), (ld, 1))
+    xd.copy_(x.to(dev))
+    X, W = values(x, sx, False)[rows.long()], values(w, sw, True)
+    ref = torch.stack([X[m] @ W[expert[m]].t() for m in range(tokens * k)])
+    size = torch.stack([X[m].abs() @ W[expert[m]].abs().t() for m in range(tokens * k)])
+    for variant in (0, mg.MOE_MATMUL_ROWS_16, mg.MOE_MATMUL_FAR_ROWS):
+        y = torch.empty(tokens * k, N, dtype=torch.float32, device=dev)
+        mg.moe_decode_matmul_fp8_experts(xd, sx.to(dev), counts.to(dev), w.to(dev), sw.to(dev), y, x_rows=rows.to(dev),
+                                         variant=variant or None)
+        torch.cuda.synchronize()
+        check(y, ref, size, K, f"far picked rows variant {variant}")
 
 
 def test_experts_matrices_beyond_4_gib(dev):
