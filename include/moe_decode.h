@@ -308,7 +308,7 @@ int moe_decode_conventional_noalloc(const void *x, const int32_t *topk_ids, cons
  * give the same bits.  Elements between the rows (ld > E) are neither read
  * nor written.
  * Limits: E <= 1024, k <= 64 and k <= E, G divides T, T * k < 2^31,
- * G <= 2^20, G * E < 2^28, strides up to 2^30.  `workspace` is device memory of at least
+ * G <= 2^19, G * E < 2^26, strides up to 2^30.  `workspace` is device memory of at least
  * moe_decode_balance_workspace() bytes, 256-byte aligned, used until the
  * launches complete (calls that may overlap in time need one each); it need
  * not be cleared.  T == 0 is a valid no-op that writes nothing. */

@@ -13,8 +13,8 @@ int check_balance(int T, int E, int k, int G) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || G <= 0) return MOE_ERR_SHAPE;
   if (E > moe::kBalMaxExperts || k > moe::kBalMaxK || T % G) return MOE_ERR_SHAPE;
   if ((long long)T * k >= (1LL << 31)) return MOE_ERR_SHAPE;
-  // a launch holds fewer than 2^32 threads: G * ceil(E / 32) workgroups of 256, G of 512
-  if (G > (1 << 20) || (long long)G * E >= (1LL << 28)) return MOE_ERR_SHAPE;
+  // a launch holds fewer than 2^32 threads: G * ceil(E / 32) workgroups of 1024, G of 512
+  if (G > (1 << 19) || (long long)G * E >= (1LL << 26)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -59,11 +59,20 @@ struct Forward {
   float* z;
   int32_t* n;
   uint32_t* ticket;
+  float* losses;
+  int32_t* counts;
+  int32_t* tokens;
   int S, E, k, G, parts;
   template <typename T, int LR, int V, int C>
   void operator()() const {
-    hipLaunchKernelGGL((moe::balance_parts_kernel<T, LR, V, C>), dim3((unsigned)(G * parts)), dim3(moe::kBalThreads), 0,
-                       st, static_cast<const T*>(logits), ld, ids, valid, psum, cnt, z, n, ticket, S, E, k, parts);
+    const dim3 grid((unsigned)(G * parts)), block(moe::kBalThreads);
+    const T* x = static_cast<const T*>(logits);
+    if (G * parts == 1)
+      hipLaunchKernelGGL((moe::balance_parts_kernel<T, LR, V, C, true>), grid, block, 0, st, x, ld, ids, valid, psum, cnt, z,
+                         n, ticket, losses, counts, tokens, S, E, k, parts);
+    else
+      hipLaunchKernelGGL((moe::balance_parts_kernel<T, LR, V, C, false>), grid, block, 0, st, x, ld, ids, valid, psum, cnt,
+                         z, n, ticket, losses, counts, tokens, S, E, k, parts);
   }
 };
 
@@ -132,10 +141,18 @@ int moe_decode_balance(const void* logits, long long ld, int dtype, const int32_
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   by_shape(dtype, whole_pieces(logits, T, E, ld, dtype), E,
-           Forward{st, logits, ld, topk_ids, valid, psum, cnt, z, n, ticket, S, E, k, G, parts});
-  hipLaunchKernelGGL(moe::balance_sum_kernel, dim3((unsigned)(G * moe::balance_splits(E))), dim3(moe::kBalSumThreads), 0,
-                     st, psum, cnt, z, n, reinterpret_cast<double*>(ws + L.dot), reinterpret_cast<double*>(ws + L.zsum),
-                     ticket, losses, counts, tokens, E, k, G, parts);
+           Forward{st, logits, ld, topk_ids, valid, psum, cnt, z, n, ticket, losses, counts, tokens, S, E, k, G, parts});
+  if (G * parts > 1) {
+    double* dot = reinterpret_cast<double*>(ws + L.dot);
+    double* zsum = reinterpret_cast<double*>(ws + L.zsum);
+    const dim3 block(moe::kBalSumThreads);
+    if (E <= 128 && parts <= 128)
+      hipLaunchKernelGGL(moe::balance_sum_kernel<128>, dim3((unsigned)G), block, 0, st, psum, cnt, z, n, dot, zsum, ticket,
+                         losses, counts, tokens, E, k, G, parts);
+    else
+      hipLaunchKernelGGL(moe::balance_sum_kernel<moe::kBalSumCols>, dim3((unsigned)(G * moe::balance_splits(E))), block, 0,
+                         st, psum, cnt, z, n, dot, zsum, ticket, losses, counts, tokens, E, k, G, parts);
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 

@@ -8,13 +8,23 @@
 // V - 1 operations in the lane and 4 (or 6) DPP steps across it.  With 16
 // lanes a row of 128 experts is two 16-byte loads per lane.
 //
-// Forward: a workgroup takes a contiguous part of one group's tokens; each
+// The next round of rows is requested before the current one is worked on.
+//
+// Forward: a workgroup takes a part of one group's tokens; each
 // lane adds up its columns' probabilities over its rows, the wavefronts' sums
 // are added in LDS in a fixed order, and the slots are counted with integer
 // LDS atomics, whose order cannot change the result.  The parts' sums go to
-// the workspace, and a second launch adds them (FP64, fixed order).
+// the workspace, and a second launch adds them (FP64, fixed order); a single
+// part (up to 256 tokens) finishes alone.
 // Backward: the same walk with f_ge in registers; the softmax is computed
 // again rather than stored (a stored one would be T E more bytes each way).
+//
+// 262144 tokens of 128 experts, FP32, 64 padded groups: forward 30 us, of them
+// 8 the second launch, both 89 us for 410 MB (4.6 TB/s; a copy of that size
+// 6.3): memory, and about 120 vector instructions for 4 rows.  More wavefronts
+// (1024 parts: the forward 52 us) or a second round requested ahead (the same)
+// do not help.  4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which
+// is their latency.
 #pragma once
 
 #include "prims.hpp"
@@ -26,16 +36,20 @@ constexpr int kBalThreads = 512;
 constexpr int kBalWaves = kBalThreads / 64;
 constexpr int kBalMaxExperts = 1024;
 constexpr int kBalMaxK = 64;
-constexpr int kBalSumThreads = 256;
-constexpr int kBalSumCols = 32;       // experts one workgroup of the second launch adds up
+constexpr int kBalSumThreads = 1024;
+constexpr int kBalSumWaves = kBalSumThreads / 64;
+constexpr int kBalSumCols = 32;       // experts that one workgroup of the second launch adds up, at least
 constexpr int kBalTargetParts = 512;  // workgroups of a pass: 2 per CU
+constexpr int kBalAhead = 1;          // rounds of rows that a wavefront has requested
+constexpr int kBalAlone = 256;        // tokens that one workgroup takes without a second launch
 
 // Parts each group's tokens are cut into: enough workgroups for the chip, at
 // least 32 tokens each.
 __host__ __device__ constexpr int balance_parts(int S, int G) {
+  if ((long long)S * G <= kBalAlone) return 1;
   const int by_chip = (kBalTargetParts + G - 1) / G;
   const int by_work = (S + 31) / 32;
-  return by_chip < by_work ? by_chip : (by_work < 1 ? 1 : by_work);
+  return by_chip < by_work ? by_chip : by_work;
 }
 
 __host__ __device__ constexpr int balance_splits(int E) { return (E + kBalSumCols - 1) / kBalSumCols; }
@@ -88,7 +102,8 @@ __device__ __forceinline__ int balance_col(int l, int v) {
 
 __device__ __forceinline__ float bf16_bits_f32(uint32_t b) { return __builtin_bit_cast(float, b << 16); }
 
-// A row's logits as FP32, -inf beyond E.
+// A row's logits.  Every load is made, of a column that exists where the lane
+// has none: a load under a condition would be waited for at its end.
 template <typename T, int LR, int V, int C>
 struct RowLoad {
   uint32_t raw[sizeof(T) == 4 || C == 1 ? V : V / 2];
@@ -96,15 +111,13 @@ struct RowLoad {
     if constexpr (C == 4) {
 #pragma unroll
       for (int g = 0; g < V / 4; ++g) {
-        const int c = balance_col<LR, 4>(l, 4 * g);
+        const int c = min(balance_col<LR, 4>(l, 4 * g), E - 4);
         if constexpr (sizeof(T) == 4) {
-          u32x4 t{{0, 0, 0, 0}};
-          if (c < E) t = *reinterpret_cast<const u32x4*>(row + c);
+          const u32x4 t = *reinterpret_cast<const u32x4*>(row + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) raw[4 * g + i] = t.v[i];
         } else {
-          uint2 t{0, 0};
-          if (c < E) t = *reinterpret_cast<const uint2*>(row + c);
+          const uint2 t = *reinterpret_cast<const uint2*>(row + c);
           raw[2 * g] = t.x;
           raw[2 * g + 1] = t.y;
         }
@@ -112,32 +125,32 @@ struct RowLoad {
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = balance_col<LR, 1>(l, v);
-        raw[v] = 0;
-        if (c < E) {
-          if constexpr (sizeof(T) == 4) raw[v] = __builtin_bit_cast(uint32_t, row[c]);
-          else raw[v] = row[c];
-        }
+        const int c = min(balance_col<LR, 1>(l, v), E - 1);
+        if constexpr (sizeof(T) == 4) raw[v] = __builtin_bit_cast(uint32_t, row[c]);
+        else raw[v] = row[c];
       }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[V], int E, int l) const {
+  // As FP32; -inf beyond E and in a row that does not count, whatever it holds.
+  __device__ __forceinline__ void values(float (&x)[V], int E, int l, bool on) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float f;
       if constexpr (sizeof(T) == 4) f = __builtin_bit_cast(float, raw[v]);
       else if constexpr (C == 4) f = bf16_bits_f32((v & 1) ? raw[v / 2] >> 16 : raw[v / 2] & 0xFFFFu);
       else f = bf16_bits_f32(raw[v]);
-      x[v] = balance_col<LR, C>(l, v) < E ? f : -__builtin_huge_valf();
+      x[v] = on & (balance_col<LR, C>(l, v) < E) ? f : -__builtin_huge_valf();
     }
   }
 };
 
-// x becomes the row's probabilities; returns its log-sum-exp.  A row of -inf
-// only: probabilities and log-sum-exp 0.  A NaN or +inf anywhere makes every
-// probability and the log-sum-exp NaN.
+// x becomes exp(x - max); `inv` the factor that makes probabilities of it;
+// returns the log-sum-exp.  A row of -inf only: all three are 0.  A NaN or +inf
+// anywhere makes every probability and the log-sum-exp NaN.  The sum lies in
+// [1, E], so the instructions' reciprocal and logarithm (1 ulp) need no care
+// for range.
 template <int LR, int V>
-__device__ __forceinline__ float row_softmax(float (&x)[V]) {
+__device__ __forceinline__ float row_softmax(float (&x)[V], float& inv) {
   float m = x[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
@@ -146,185 +159,298 @@ __device__ __forceinline__ float row_softmax(float (&x)[V]) {
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    x[v] = __expf(x[v] - m);
+    x[v] = __builtin_amdgcn_exp2f((x[v] - m) * 1.44269504f);
     s += x[v];
   }
   s = row_sum<LR>(s);
-  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-  for (int v = 0; v < V; ++v) x[v] *= inv;
-  return s == 0.0f ? 0.0f : m + __logf(s);
+  inv = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+  return s == 0.0f ? 0.0f : m + __builtin_amdgcn_logf(s) * 0.693147181f;
 }
 
-// One part: tokens [first, last) of group g.
-template <typename T, int LR, int V, int C>
+// Sum over the 64 lanes in a fixed order; every lane gets it.
+template <typename A>
+__device__ __forceinline__ A wave_sum(A v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// One part of group g: blocks of 8 wavefronts' rows, `parts` blocks apart.  ALONE: there is no other (one
+// group, one part), and losses, counts and tokens are written here.
+template <typename T, int LR, int V, int C, bool ALONE>
 __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
     const T* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const uint8_t* __restrict__ valid,
     float* __restrict__ psum, int32_t* __restrict__ cnt, float* __restrict__ zpart, int32_t* __restrict__ npart,
-    uint32_t* __restrict__ ticket, int S, int E, int k, int parts) {
+    uint32_t* __restrict__ ticket, float* __restrict__ losses, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens, int S, int E, int k, int parts) {
   constexpr int RW = 64 / LR;                // rows a wavefront works on at a time
   constexpr int kCols = LR * V;
   __shared__ float sp[kBalWaves * kCols];
   __shared__ int32_t hist[kCols];
-  __shared__ float sz[kBalWaves * RW];
-  __shared__ int32_t sn[kBalWaves * RW];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  __shared__ float sz[kBalWaves];
+  __shared__ int32_t sn[kBalWaves];
+  __shared__ double sd[kBalWaves];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane % LR, rw = lane / LR;
   const int g = blockIdx.x / parts, part = blockIdx.x - g * parts;
-  const int per = (S + parts - 1) / parts;
-  const int first = min(part * per, S), last = min(first + per, S);
   const long long base = (long long)g * S;
+  const T* glogits = logits + base * ld;
+  const int32_t* gids = ids + base * k;
+  const uint32_t all = valid ? 0u : 1u;   // every token counts
+  const uint8_t* gvalid = valid ? valid + base : reinterpret_cast<const uint8_t*>(gids);   // any byte: not looked at
+
+  struct Rows {
+    RowLoad<T, LR, V, C> r;
+    uint32_t on;
+    int id;   // this lane's slot of its row (l < k)
+  } rows[kBalAhead];
+  auto request = [&](Rows& q, int t) {
+    const int c = min(t, S - 1);
+    q.r.load(glogits + (long long)c * ld, E, l);
+    q.on = gvalid[c];
+    q.id = gids[c * k + min(l, k - 1)];
+  };
+  auto count = [&](bool counted, int e) {
+    if (counted & ((unsigned)e < (unsigned)E)) atomicAdd(&hist[e], 1);
+  };
+  // Round i of the part: the workgroups' blocks of one round lie side by side,
+  // and the groups begin at different rounds; with a range of its own for
+  // each part all of them read and wrote the same memory channels at a time
+  // (262144 tokens of 128 experts in 64
+  // groups: both passes 96 against 90 us).
+  constexpr int kStep = kBalWaves * RW;
+  const int rounds = (S + parts * kStep - 1) / (parts * kStep);
+  auto token = [&](int i) {
+    int r = i + g % rounds;
+    r -= r >= rounds ? rounds : 0;
+    return (r * parts + part) * kStep + w * RW + rw;
+  };
+#pragma unroll
+  for (int u = 0; u < kBalAhead; ++u) request(rows[u], token(min(u, rounds - 1)));
   for (int i = tid; i < kCols; i += kBalThreads) hist[i] = 0;
-  if (blockIdx.x == 0 && tid == 0) *ticket = 0;
+  if (!ALONE && blockIdx.x == 0 && tid == 0) *ticket = 0;
   __syncthreads();
 
-  // slots of valid tokens
-  const int32_t* gids = ids + base * k;
-  for (int i = first * k + tid; i < last * k; i += kBalThreads) {
-    const bool on = !valid || valid[base + i / k];
-    const int e = gids[i];
-    if (on && (unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+  if (k > LR) {   // slots that a row's lanes do not cover
+    const int more = k - LR;
+    for (int r = 0; r < rounds; ++r)
+      for (int i = tid; i < kStep * more; i += kBalThreads) {
+        const int t = (r * parts + part) * kStep + i / more, s = LR + i % more;
+        if (t < S) count(!valid || gvalid[t], gids[t * k + s]);
+      }
   }
-
   float P[V], zacc = 0.0f;
   int nacc = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) P[v] = 0.0f;
-  for (int t0 = first; t0 < last; t0 += kBalWaves * RW) {
-    const int t = t0 + w * RW + rw;
-    const bool on = t < last && (!valid || valid[base + t]);
-    RowLoad<T, LR, V, C> r;
-    r.load(logits + (base + min(t, last - 1)) * ld, E, l);
-    float x[V];
-    r.values(x, E, l);
-    const float z = row_softmax<LR, V>(x);
-    // selects, not products: an invalid row may hold NaN
+  for (int i = 0; i < rounds; i += kBalAhead) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) P[v] += on ? x[v] : 0.0f;
-    zacc += on ? z * z : 0.0f;
-    nacc += on ? 1 : 0;
+    for (int u = 0; u < kBalAhead; ++u) {
+      if (i + u >= rounds) break;
+      const int t = token(i + u);
+      const bool now = (t < S) & ((rows[u].on | all) != 0u);   // no branch: a load waited for in one is waited for at its end
+      float x[V], inv;
+      rows[u].r.values(x, E, l, now);
+      count(now & (l < k), rows[u].id);
+      request(rows[u], token(min(i + u + kBalAhead, rounds - 1)));   // behind the last round: that one again
+      __builtin_amdgcn_sched_barrier(0);         // before the work on this round, not after it
+      const float z = row_softmax<LR, V>(x, inv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) P[v] = __builtin_fmaf(x[v], inv, P[v]);
+      zacc = __builtin_fmaf(z, z, zacc);
+      nacc += now ? 1 : 0;
+    }
   }
   // the wavefront's row groups first (lanes l, l + LR, ...), then the wavefronts
+  if constexpr (LR == 16) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if constexpr (LR == 16) {
+    for (int v = 0; v < V; ++v) {
       P[v] += __shfl_xor(P[v], 16);
       P[v] += __shfl_xor(P[v], 32);
     }
-    if (rw == 0) sp[w * kCols + balance_col<LR, C>(l, v)] = P[v];
+    zacc += __shfl_xor(zacc, 16);
+    zacc += __shfl_xor(zacc, 32);
+    nacc += __shfl_xor(nacc, 16);
+    nacc += __shfl_xor(nacc, 32);
   }
-  if (l == 0) {
-    sz[w * RW + rw] = zacc;
-    sn[w * RW + rw] = nacc;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (rw == 0) sp[w * kCols + balance_col<LR, C>(l, v)] = P[v];
+  if (lane == 0) {
+    sz[w] = zacc;
+    sn[w] = nacc;
   }
   __syncthreads();
+  double dot = 0.0;
   for (int c = tid; c < E; c += kBalThreads) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kBalWaves; ++i) s += sp[i * kCols + c];
-    psum[(size_t)blockIdx.x * E + c] = s;
-    cnt[(size_t)blockIdx.x * E + c] = hist[c];
+    if constexpr (ALONE) {
+      counts[c] = hist[c];
+      dot += (double)s * (double)hist[c];
+    } else {
+      psum[(size_t)blockIdx.x * E + c] = s;
+      cnt[(size_t)blockIdx.x * E + c] = hist[c];
+    }
+  }
+  if constexpr (ALONE) {
+    dot = wave_sum(dot);
+    if (lane == 0) sd[w] = dot;
+    __syncthreads();
   }
   if (tid == 0) {
     float z = 0.0f;
     int n = 0;
-    for (int i = 0; i < kBalWaves * RW; ++i) {
+    dot = 0.0;
+#pragma unroll
+    for (int i = 0; i < kBalWaves; ++i) {
       z += sz[i];
       n += sn[i];
+      if (ALONE) dot += sd[i];
     }
-    zpart[blockIdx.x] = z;
-    npart[blockIdx.x] = n;
+    if constexpr (ALONE) {
+      losses[0] = n > 0 ? (float)(dot * (double)E / ((double)k * (double)n * (double)n)) : 0.0f;
+      losses[1] = n > 0 ? (float)((double)z / (double)n) : 0.0f;
+      tokens[0] = tokens[1] = n;
+    } else {
+      zpart[blockIdx.x] = z;
+      npart[blockIdx.x] = n;
+    }
   }
 }
 
 // Sum over the workgroup in a fixed order; every thread gets it.
-template <int THREADS, typename A>
+template <typename A>
 __device__ __forceinline__ A block_sum(A v, A* scratch, int tid) {
-  scratch[tid] = v;
+  v = wave_sum(v);
+  if ((tid & 63) == 0) scratch[tid >> 6] = v;
   __syncthreads();
+  v = scratch[0];
 #pragma unroll
-  for (int o = THREADS / 2; o > 0; o >>= 1) {
-    if (tid < o) scratch[tid] += scratch[tid + o];
-    __syncthreads();
-  }
-  const A s = scratch[0];
+  for (int i = 1; i < kBalSumWaves; ++i) v += scratch[i];
   __syncthreads();
-  return s;
+  return v;
 }
 
-// Second launch, one workgroup per (group, 32 experts): adds the parts, writes
+// Second launch, one workgroup per (group, COLS experts): adds the parts, writes
 // the group's counts, and leaves sum_e c_ge sum_t p_te in the workspace.  The
 // workgroup that finishes last adds those up to the two losses; which one that
-// is does not change the order of the sum.
+// is does not change the order of the sum.  32 experts a workgroup spread many
+// parts over more workgroups; 128 make it one workgroup for one group, with
+// nothing to wait for (128 parts of 128 experts: 4.2 against 6.8 us).
+template <int COLS>
 __global__ __launch_bounds__(kBalSumThreads) void balance_sum_kernel(
     const float* __restrict__ psum, const int32_t* __restrict__ cnt, const float* __restrict__ zpart,
     const int32_t* __restrict__ npart, double* __restrict__ dot, double* __restrict__ zsum,
     uint32_t* __restrict__ ticket, float* __restrict__ losses, int32_t* __restrict__ counts,
     int32_t* __restrict__ tokens, int E, int k, int G, int parts) {
-  constexpr int kSlices = kBalSumThreads / kBalSumCols;
+  constexpr int kSlices = kBalSumThreads / COLS, kBatch = COLS == 32 ? 4 : 16;
+  static_assert(COLS == 32 || COLS == 128);
   __shared__ double sd[kBalSumThreads];
   __shared__ int32_t si[kBalSumThreads];
+  constexpr int kZWave = kBalSumWaves - 1;
+  __shared__ double sdot[(COLS + 63) / 64];
+  __shared__ double sz;
+  __shared__ int32_t sn;
   __shared__ bool is_last;
-  const int tid = threadIdx.x, splits = balance_splits(E);
+  const int tid = threadIdx.x, splits = (E + COLS - 1) / COLS;
   const int g = blockIdx.x / splits, sp = blockIdx.x - g * splits;
-  const int c = sp * kBalSumCols + tid % kBalSumCols, slice = tid / kBalSumCols;
+  const int c = sp * COLS + tid % COLS, slice = tid / COLS;
+  const float* gp = psum + (size_t)g * parts * E + min(c, E - 1);
+  const int32_t* gc = cnt + (size_t)g * parts * E + min(c, E - 1);
   double p = 0.0;
   int n = 0;
-  if (c < E)
-    for (int i = slice; i < parts; i += kSlices) {
-      p += (double)psum[((size_t)g * parts + i) * E + c];
-      n += cnt[((size_t)g * parts + i) * E + c];
+  for (int i = slice; i < parts; i += kBatch * kSlices) {   // kBatch parts' loads at a time
+    float a[kBatch];
+    int b[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = min(i + u * kSlices, parts - 1);
+      a[u] = gp[(size_t)j * E];
+      b[u] = gc[(size_t)j * E];
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const bool in = i + u * kSlices < parts;
+      p += in ? (double)a[u] : 0.0;
+      n += in ? b[u] : 0;
+    }
+  }
   sd[tid] = p;
   si[tid] = n;
-  __syncthreads();
-  p = 0.0;
-  n = 0;
-  if (tid < kBalSumCols) {
-    for (int s = 0; s < kSlices; ++s) {
-      p += sd[s * kBalSumCols + tid];
-      n += si[s * kBalSumCols + tid];
-    }
-    if (c < E) counts[(size_t)g * E + c] = n;
-  }
-  __syncthreads();
-  const double d = block_sum<kBalSumThreads>(tid < kBalSumCols ? p * (double)n : 0.0, sd, tid);
-  if (sp == 0) {
-    double z = 0.0;
-    int v = 0;
-    for (int i = tid; i < parts; i += kBalSumThreads) {
+  double z = 0.0;   // the group's z and valid tokens: the last wavefront of its first workgroup
+  int v = 0;
+  if (sp == 0 && (tid >> 6) == kZWave)
+    for (int i = tid & 63; i < parts; i += 64) {
       z += (double)zpart[(size_t)g * parts + i];
       v += npart[(size_t)g * parts + i];
     }
-    z = block_sum<kBalSumThreads>(z, sd, tid);
-    v = block_sum<kBalSumThreads>(v, si, tid);
-    if (tid == 0) {
-      zsum[g] = z;
-      tokens[g] = v;
+  __syncthreads();
+  double d = 0.0;
+  if (tid < COLS) {
+    p = 0.0;
+    n = 0;
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+      p += sd[s * COLS + tid];
+      n += si[s * COLS + tid];
+    }
+    if (c < E) {
+      counts[(size_t)g * E + c] = n;
+      d = p * (double)n;
     }
   }
+  if (tid < COLS || tid < 64) {
+    d = wave_sum(d);
+    if ((tid & 63) == 0) sdot[tid >> 6] = d;
+  }
+  if ((tid >> 6) == kZWave) {
+    z = wave_sum(z);
+    v = wave_sum(v);
+    if ((tid & 63) == 0) {
+      sz = z;
+      sn = v;
+    }
+  }
+  __syncthreads();
+  d = sdot[0];
+  if constexpr (COLS > 64) d += sdot[1];
+  if (gridDim.x == 1) {
+    if (tid == 0) {
+      const double m = sn > 0 ? (double)sn : 1.0;
+      losses[0] = (float)(d * (double)E / ((double)k * m * m));
+      losses[1] = (float)(sz / m);
+      tokens[0] = tokens[1] = sn;
+    }
+    return;
+  }
+  // one thread publishes what the last workgroup reads (agent scope: the workgroups run on different XCDs)
   if (tid == 0) {
-    dot[blockIdx.x] = d;
-    __threadfence();
+    __hip_atomic_store(&dot[blockIdx.x], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (sp == 0) {
+      __hip_atomic_store(&zsum[g], sz, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&tokens[g], sn, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     is_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   }
   __syncthreads();
   if (!is_last) return;
-  __threadfence();
-  double bal = 0.0, z = 0.0;
+  double bal = 0.0;
   int N = 0;
+  z = 0.0;
   for (int i = tid; i < G; i += kBalSumThreads) {
-    const int v = __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int m = __hip_atomic_load(&tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     double s = 0.0;
     for (int j = 0; j < splits; ++j)
       s += __hip_atomic_load(&dot[(size_t)i * splits + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (v > 0) bal += s * (double)E / ((double)k * (double)v * (double)v);
+    if (m > 0) bal += s * (double)E / ((double)k * (double)m * (double)m);
     z += __hip_atomic_load(&zsum[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    N += v;
+    N += m;
   }
-  bal = block_sum<kBalSumThreads>(bal, sd, tid);
-  z = block_sum<kBalSumThreads>(z, sd, tid);
-  N = block_sum<kBalSumThreads>(N, si, tid);
+  bal = block_sum(bal, sd, tid);
+  z = block_sum(z, sd, tid);
+  N = block_sum(N, si, tid);
   if (tid == 0) {
     losses[0] = (float)(bal / (double)G);
     losses[1] = N > 0 ? (float)(z / (double)N) : 0.0f;
@@ -338,12 +464,35 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
     const int32_t* __restrict__ tokens, const float* __restrict__ grad_losses, T* __restrict__ dlogits, long long ld_d,
     int S, int E, int k, int G, int parts) {
   constexpr int RW = 64 / LR;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane % LR, rw = lane / LR;
   const int g = blockIdx.x / parts, part = blockIdx.x - g * parts;
-  const int per = (S + parts - 1) / parts;
-  const int first = min(part * per, S), last = min(first + per, S);
   const long long base = (long long)g * S;
+  struct Rows {
+    RowLoad<T, LR, V, C> r;
+    uint32_t on;
+  } rows[kBalAhead];
+  const uint32_t all = valid ? 0u : 1u;   // every token counts
+  const uint8_t* gvalid = valid ? valid + base : reinterpret_cast<const uint8_t*>(logits);   // any byte: not looked at
+  auto request = [&](Rows& q, int t) {
+    const int c = min(t, S - 1);
+    q.r.load(logits + (base + c) * ld, E, l);
+    q.on = gvalid[valid ? c : 0];
+  };
+  // Round i of the part: the workgroups' blocks of one round lie side by side,
+  // and the groups begin at different rounds; with a range of its own for
+  // each part all of them read and wrote the same memory channels at a time
+  // (262144 tokens of 128 experts in 64
+  // groups: both passes 96 against 90 us).
+  constexpr int kStep = kBalWaves * RW;
+  const int rounds = (S + parts * kStep - 1) / (parts * kStep);
+  auto token = [&](int i) {
+    int r = i + g % rounds;
+    r -= r >= rounds ? rounds : 0;
+    return (r * parts + part) * kStep + w * RW + rw;
+  };
+#pragma unroll
+  for (int u = 0; u < kBalAhead; ++u) request(rows[u], token(min(u, rounds - 1)));
   const float n = (float)max(tokens[g], 1), N = (float)max(tokens[G], 1);
   const float fb = grad_losses[0] * ((float)E / ((float)G * (float)k * n * n));
   const float zc = grad_losses[1] * (2.0f / N);
@@ -351,46 +500,51 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = balance_col<LR, C>(l, v);
-    F[v] = c < E ? fb * (float)counts[(size_t)g * E + c] : 0.0f;
+    F[v] = (float)counts[(size_t)g * E + min(c, E - 1)];
   }
-  for (int t0 = first; t0 < last; t0 += kBalWaves * RW) {
-    const int t = t0 + w * RW + rw;
-    const bool in = t < last;
-    const bool on = in && (!valid || valid[base + t]);
-    RowLoad<T, LR, V, C> r;
-    r.load(logits + (base + min(t, last - 1)) * ld, E, l);
-    float x[V];
-    r.values(x, E, l);
-    const float z = row_softmax<LR, V>(x);
-    float dot = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) dot += x[v] * F[v];
-    dot = row_sum<LR>(dot);
-    const float zt = zc * z - dot;
+  for (int v = 0; v < V; ++v) F[v] = balance_col<LR, C>(l, v) < E ? fb * F[v] : 0.0f;
+  for (int i = 0; i < rounds; i += kBalAhead) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = on ? x[v] * (F[v] + zt) : 0.0f;
-    if (!in) continue;
-    T* out = dlogits + (base + t) * ld_d;
-    if constexpr (C == 4) {
+    for (int u = 0; u < kBalAhead; ++u) {
+      if (i + u >= rounds) break;
+      const int t = token(i + u);
+      const bool in = t < S, now = in & ((rows[u].on | all) != 0u);
+      float x[V], inv;
+      rows[u].r.values(x, E, l, now);
+      request(rows[u], token(min(i + u + kBalAhead, rounds - 1)));   // behind the last round: that one again
+      __builtin_amdgcn_sched_barrier(0);         // before the work on this round, not after it
+      const float z = row_softmax<LR, V>(x, inv);
+      float dot = 0.0f;
 #pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const int c = balance_col<LR, 4>(l, 4 * q);
-        if (c >= E) continue;
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(out + c) = float4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-        } else {
-          *reinterpret_cast<uint2*>(out + c) =
-              uint2{f32_to_bf16_rne(x[4 * q]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 1]) << 16,
-                    f32_to_bf16_rne(x[4 * q + 2]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 3]) << 16};
+      for (int v = 0; v < V; ++v) dot = __builtin_fmaf(x[v], F[v], dot);
+      dot = row_sum<LR>(dot) * inv;
+      const float zt = zc * z - dot;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = now ? x[v] * inv * (F[v] + zt) : 0.0f;
+      if (!in) continue;
+      T* out = dlogits + (base + t) * ld_d;
+      if constexpr (C == 4) {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+          const int c = balance_col<LR, 4>(l, 4 * q);
+          if (c >= E) continue;
+          if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(out + c) = float4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+          } else {
+            *reinterpret_cast<uint2*>(out + c) =
+                uint2{f32_to_bf16_rne(x[4 * q]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 1]) << 16,
+                      f32_to_bf16_rne(x[4 * q + 2]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 3]) << 16};
+          }
         }
-      }
-    } else {
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = balance_col<LR, 1>(l, v);
-        if (c < E) {
-          if constexpr (sizeof(T) == 4) out[c] = x[v];
-          else out[c] = f32_to_bf16_rne(x[v]);
+        for (int v = 0; v < V; ++v) {
+          const int c = balance_col<LR, 1>(l, v);
+          if (c < E) {
+            if constexpr (sizeof(T) == 4) out[c] = x[v];
+            else out[c] = f32_to_bf16_rne(x[v]);
+          }
         }
       }
     }

@@ -20,20 +20,26 @@ size_t row_bytes(int M, int n, long long ld, size_t size) {
 }
 bool stride_ok(int M, int n, long long ld) { return M <= 1 || (ld >= n && ld <= kMaxStride); }
 
+template <typename T, bool SWIGLU, int FORM>
+void go_quantize(hipStream_t st, const void* x, long long ldx, uint8_t* q, float* s, int units, int K, int nb, bool pow2) {
+  constexpr int per = moe::kQuantThreads / moe::kQuantLanes;
+  const uint32_t magic = (uint32_t)(((1ULL << 32) + (unsigned)nb - 1) / (unsigned)nb);   // nb = 1: not used
+  hipLaunchKernelGGL((moe::quantize_kernel<T, SWIGLU, FORM>), dim3((unsigned)((units + per - 1) / per)),
+                     dim3(moe::kQuantThreads), 0, st, static_cast<const T*>(x), ldx, q, s, units, K, nb, magic, pow2);
+}
+template <typename T, bool SWIGLU>
+void pick_quantize(int form, hipStream_t st, const void* x, long long ldx, uint8_t* q, float* s, int units, int K, int nb,
+                   bool pow2) {
+  if (form == moe::kQuantWhole) go_quantize<T, SWIGLU, moe::kQuantWhole>(st, x, ldx, q, s, units, K, nb, pow2);
+  else if (form == moe::kQuantPieces) go_quantize<T, SWIGLU, moe::kQuantPieces>(st, x, ldx, q, s, units, K, nb, pow2);
+  else go_quantize<T, SWIGLU, moe::kQuantElements>(st, x, ldx, q, s, units, K, nb, pow2);
+}
 template <typename T>
 void launch_quantize(hipStream_t st, const void* x, long long ldx, uint8_t* q, float* s, int units, int K, int nb,
-                     int flags, bool whole) {
-  constexpr int per = moe::kQuantThreads / moe::kQuantLanes;
-  const unsigned blocks = (unsigned)((units + per - 1) / per);
-  const dim3 grid(blocks < 65536u ? blocks : 65536u);
+                     int flags, int form) {
   const bool pow2 = flags & MOE_QUANT_POW2;
-  const T* xt = static_cast<const T*>(x);
-  if (flags & MOE_QUANT_SWIGLU)
-    hipLaunchKernelGGL((moe::quantize_kernel<T, true>), grid, dim3(moe::kQuantThreads), 0, st, xt, ldx, q, s, units, K, nb,
-                       pow2, whole);
-  else
-    hipLaunchKernelGGL((moe::quantize_kernel<T, false>), grid, dim3(moe::kQuantThreads), 0, st, xt, ldx, q, s, units, K,
-                       nb, pow2, whole);
+  if (flags & MOE_QUANT_SWIGLU) pick_quantize<T, true>(form, st, x, ldx, q, s, units, K, nb, pow2);
+  else pick_quantize<T, false>(form, st, x, ldx, q, s, units, K, nb, pow2);
 }
 
 // ---------------------------------------------------------------- products
@@ -217,13 +223,13 @@ int moe_decode_quantize_fp8(const void* x, long long ldx, int dtype, uint8_t* q,
   if (!aligned(x, es) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
   const size_t xb = row_bytes(M, cols, ldx, es), qb = (size_t)M * K, sb = (size_t)M * nb * 4;
   if (overlaps(q, qb, x, xb) || overlaps(scales, sb, x, xb) || overlaps(q, qb, scales, sb)) return MOE_ERR_ALIAS;
-  // whole pieces of 8 elements: 16-byte loads, 8-byte stores
-  const bool whole = K % 8 == 0 && (M == 1 || (ldx * (long long)es) % 16 == 0) && aligned(x, 16) && aligned(q, 8);
+  const bool pieces = K % 8 == 0 && (M == 1 || (ldx * (long long)es) % 16 == 0) && aligned(x, 16) && aligned(q, 8);
+  const int form = !pieces ? moe::kQuantElements : K % moe::kQuantBlock ? moe::kQuantPieces : moe::kQuantWhole;
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (dtype == MOE_F32) launch_quantize<float>(st, x, ldx, q, scales, M * nb, K, nb, flags, whole);
-  else if (dtype == MOE_BF16) launch_quantize<uint16_t>(st, x, ldx, q, scales, M * nb, K, nb, flags, whole);
-  else launch_quantize<moe::f16_t>(st, x, ldx, q, scales, M * nb, K, nb, flags, whole);
+  if (dtype == MOE_F32) launch_quantize<float>(st, x, ldx, q, scales, M * nb, K, nb, flags, form);
+  else if (dtype == MOE_BF16) launch_quantize<uint16_t>(st, x, ldx, q, scales, M * nb, K, nb, flags, form);
+  else launch_quantize<moe::f16_t>(st, x, ldx, q, scales, M * nb, K, nb, flags, form);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
