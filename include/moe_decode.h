@@ -311,7 +311,8 @@ int moe_decode_conventional_noalloc(const void *x, const int32_t *topk_ids, cons
  * G <= 2^19, G * E < 2^26, strides up to 2^30.  `workspace` is device memory of at least
  * moe_decode_balance_workspace() bytes, 256-byte aligned, used until the
  * launches complete (calls that may overlap in time need one each); it need
- * not be cleared.  T == 0 is a valid no-op that writes nothing. */
+ * not be cleared, and where that says 0 bytes (one group of up to 256 tokens)
+ * it is not looked at.  T == 0 is a valid no-op that writes nothing. */
 #define MOE_F32 0
 #define MOE_BF16 1
 #define MOE_F16 2

@@ -12,6 +12,7 @@ raises here instead of being read out of bounds on the device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -378,6 +379,7 @@ def _call(where, fn, device, stream, *args):
         raise MoeDecodeError(rc, where)
 
 
+@functools.lru_cache(maxsize=256)
 def moe_decode_balance_workspace(T, E, k, G=1):
     """Bytes of device workspace moe_decode_balance needs."""
     n = ctypes.c_size_t()
@@ -399,15 +401,16 @@ def moe_decode_balance(logits, topk_ids, losses, counts, tokens, valid=None, wor
     k, G = topk_ids.shape[-1], counts.shape[0]
     dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
     ld = _rows(logits, "logits", d, T, E)
-    if workspace is None:
+    n = moe_decode_balance_workspace(T, E, k, G) if workspace is None else workspace.numel()
+    if workspace is None and n:
         if stream is not None:
             raise ValueError("moe_decode_balance on a given stream needs a workspace")
-        workspace = _torch.empty(moe_decode_balance_workspace(T, E, k, G), dtype=_u8, device=logits.device)
-    n = workspace.numel()
+        workspace = _torch.empty(n, dtype=_u8, device=logits.device)
     _call("moe_decode_balance", L.moe_decode_balance, d, stream, logits.data_ptr(), ld, dt,
           _flat(topk_ids, "topk_ids", d, T * k, _i32), None if valid is None else _flat(valid, "valid", d, T, _flags),
           _flat(losses, "losses", d, 2, _f32), _flat(counts, "counts", d, G * E, _i32),
-          _flat(tokens, "tokens", d, G + 1, _i32), _flat(workspace, "workspace", d, n, _u8), n, T, E, k, G)
+          _flat(tokens, "tokens", d, G + 1, _i32),
+          None if workspace is None else _flat(workspace, "workspace", d, n, _u8), n, T, E, k, G)
     return losses, counts, tokens
 
 

@@ -18,6 +18,9 @@ int check_balance(int T, int E, int k, int G) {
   return MOE_OK;
 }
 
+// One workgroup does it all, without a workspace.
+bool alone(int T, int G) { return G * moe::balance_parts(T / G, G) == 1; }
+
 size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 // A row stride the byte range below cannot overflow with.
@@ -67,7 +70,7 @@ struct Forward {
   void operator()() const {
     const dim3 grid((unsigned)(G * parts)), block(moe::kBalThreads);
     const T* x = static_cast<const T*>(logits);
-    if (G * parts == 1)
+    if (parts == 1 && G == 1)
       hipLaunchKernelGGL((moe::balance_parts_kernel<T, LR, V, C, true>), grid, block, 0, st, x, ld, ids, valid, psum, cnt, z,
                          n, ticket, losses, counts, tokens, S, E, k, parts);
     else
@@ -103,7 +106,7 @@ int moe_decode_balance_workspace(int T, int E, int k, int G, size_t* bytes) {
   const int rc = check_balance(T, E, k, G);
   if (rc) return rc;
   if (!bytes) return MOE_ERR_NULL;
-  *bytes = T ? moe::BalanceLayout(T / G, E, G).total : 0;
+  *bytes = T == 0 || alone(T, G) ? 0 : moe::BalanceLayout(T / G, E, G).total;
   return MOE_OK;
 }
 
@@ -115,16 +118,18 @@ int moe_decode_balance(const void* logits, long long ld, int dtype, const int32_
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!stride_ok(T, E, ld)) return MOE_ERR_SHAPE;
-  if (!logits || !topk_ids || !losses || !counts || !tokens || !workspace) return MOE_ERR_NULL;
+  const bool single = alone(T, G);
+  if (single) workspace = nullptr;
+  if (!logits || !topk_ids || !losses || !counts || !tokens || (!single && !workspace)) return MOE_ERR_NULL;
   if (!aligned(logits, dtype_size(dtype)) || !aligned(topk_ids, 4) || !aligned(losses, 4) || !aligned(counts, 4) ||
       !aligned(tokens, 4) || !aligned(workspace, 256))
     return MOE_ERR_ALIGN;
   const moe::BalanceLayout L(T / G, E, G);
-  if (workspace_bytes < L.total) return MOE_ERR_ARG;
+  if (!single && workspace_bytes < L.total) return MOE_ERR_ARG;
   const void* in[] = {logits, topk_ids, valid};
   const size_t inb[] = {row_bytes(T, E, ld, dtype), (size_t)T * k * 4, valid ? (size_t)T : 0};
   const void* out[] = {losses, counts, tokens, workspace};
-  const size_t outb[] = {8, (size_t)G * E * 4, ((size_t)G + 1) * 4, L.total};
+  const size_t outb[] = {8, (size_t)G * E * 4, ((size_t)G + 1) * 4, single ? 0 : L.total};
   for (int o = 0; o < 4; ++o) {
     for (int i = 0; i < 3; ++i)
       if (overlaps(out[o], outb[o], in[i], inb[i])) return MOE_ERR_ALIAS;
@@ -142,7 +147,7 @@ int moe_decode_balance(const void* logits, long long ld, int dtype, const int32_
   (void)hipGetLastError();
   by_shape(dtype, whole_pieces(logits, T, E, ld, dtype), E,
            Forward{st, logits, ld, topk_ids, valid, psum, cnt, z, n, ticket, losses, counts, tokens, S, E, k, G, parts});
-  if (G * parts > 1) {
+  if (!single) {
     double* dot = reinterpret_cast<double*>(ws + L.dot);
     double* zsum = reinterpret_cast<double*>(ws + L.zsum);
     const dim3 block(moe::kBalSumThreads);

@@ -20,7 +20,7 @@ def P(v):
 
 
 def balance(logits=at(0), ld=128, dtype=mg.MOE_F32, ids=at(1), valid=0, losses=at(2), counts=at(3), tokens=at(4),
-            ws=at(5), ws_bytes=None, T=64, E=128, k=8, G=1):
+            ws=at(5), ws_bytes=None, T=640, E=128, k=8, G=1):
     if ws_bytes is None:
         n = ctypes.c_size_t()
         mg.lib().moe_decode_balance_workspace(T, E, k, G, ctypes.byref(n))   # leaves 0 where it refuses
@@ -30,7 +30,7 @@ def balance(logits=at(0), ld=128, dtype=mg.MOE_F32, ids=at(1), valid=0, losses=a
 
 
 def backward(logits=at(0), ld=128, dtype=mg.MOE_F32, valid=0, counts=at(1), tokens=at(2), grad=at(3), d=at(4), ld_d=128,
-             T=64, E=128, k=8, G=1):
+             T=640, E=128, k=8, G=1):
     return mg.lib().moe_decode_balance_backward(P(logits), ld, dtype, P(valid), P(counts), P(tokens), P(grad), P(d), ld_d,
                                                 T, E, k, G, None)
 
@@ -58,7 +58,7 @@ def experts(x=at(0), ldx=2048, sx=at(1), rows=at(5), counts=at(6), w=at(2), sw=a
 @pytest.mark.parametrize("fn", [balance, backward])
 def test_balance_shapes(fn):
     for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=65, E=128), dict(k=9, E=8, ld=8), dict(E=1025, ld=1025), dict(G=0),
-                dict(G=5), dict(ld=127), dict(T=1 << 30, k=2), dict(T=1 << 21, G=1 << 21), dict(T=1 << 19, G=1 << 19, E=512, ld=512),
+                dict(G=7), dict(ld=127), dict(T=1 << 30, k=2), dict(T=1 << 21, G=1 << 21), dict(T=1 << 19, G=1 << 19, E=512, ld=512),
                 dict(ld=(1 << 30) + 128)):
         if fn is backward and "ld" in bad:
             bad.setdefault("ld_d", max(bad["ld"], 0))
@@ -98,6 +98,8 @@ def test_empty_calls_do_nothing():
     assert matmul(M=0, x=0, sx=0, w=0, sw=0, y=0) == mg.MOE_OK
     assert experts(M=0, X=0, x=0, sx=0, rows=0, counts=0, w=0, sw=0, y=0) == mg.MOE_OK
     assert mg.moe_decode_balance_workspace(0, 128, 8) == 0
+    assert mg.moe_decode_balance_workspace(256, 128, 8) == 0 < mg.moe_decode_balance_workspace(257, 128, 8)
+    assert mg.moe_decode_balance_workspace(256, 128, 8, 2) > 0
 
 
 def test_quantize_refusals():

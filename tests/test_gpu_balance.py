@@ -113,7 +113,8 @@ def check(got, ref, dtype, what):
 SHAPES = [
     # G, S, E, k, dtype, mask, columns between the rows
     (1, 1, 1, 1, torch.float32, None, 0), (1, 1, 128, 8, torch.float32, None, 0), (2, 3, 5, 2, torch.float32, "random", 0),
-    (1, 64, 128, 8, torch.float32, None, 0), (1, 64, 128, 8, torch.bfloat16, None, 0),
+    (1, 64, 128, 8, torch.float32, None, 0), (1, 64, 128, 8, torch.bfloat16, None, 0), (1, 256, 128, 20, torch.float32, "random", 0),
+    (1, 257, 96, 17, torch.bfloat16, "random", 0), (1, 200, 700, 8, torch.float32, "random", 0), (1, 129, 1, 1, torch.float32, "empty", 0),
     (3, 37, 100, 6, torch.bfloat16, "random", 0), (3, 37, 100, 6, torch.float32, "random", 4),
     (1, 1000, 256, 8, torch.float32, "random", 3), (4, 513, 65, 64, torch.float32, "one group empty", 0),
     (5, 33, 1000, 8, torch.float32, None, 0), (5, 33, 1000, 8, torch.bfloat16, "random", 24), (2, 150, 1024, 64, torch.float32, None, 0),
@@ -312,8 +313,10 @@ def test_refusals(dev):
         mg.moe_decode_balance(*ok, valid=torch.ones(9, dtype=torch.bool, device=dev))
     with pytest.raises(ValueError):
         mg.moe_decode_balance(*ok, valid=torch.ones(10, device=dev))
+    mg.moe_decode_balance(*ok, workspace=torch.empty(16, dtype=torch.uint8, device=dev))   # so few tokens need none
+    many = (torch.zeros(300, 16, device=dev), torch.zeros(300, 2, dtype=torch.int32, device=dev)) + ok[2:]
     with pytest.raises(mg.MoeDecodeError):
-        mg.moe_decode_balance(*ok, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+        mg.moe_decode_balance(*many, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
     with pytest.raises(mg.MoeDecodeError):   # 3 groups do not divide 10 tokens
         mg.moe_decode_balance(logits, ids, losses, torch.empty(3, 16, dtype=torch.int32, device=dev),
                               torch.empty(4, dtype=torch.int32, device=dev))
