@@ -189,7 +189,8 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
       !aligned(x_rows, 4) || !aligned(counts, 4))
     return MOE_ERR_ALIGN;
   moe::MatmulArgs a{x, ldx, sx, x_rows, counts, w, sw, y, ldy, X, M, N, K, experts ? E : 0, (K + 127) / 128,
-                    (N + 127) / 128, N % 4 == 0 && ldy % 4 == 0 && aligned(y, 4 * os)};
+                    (N + 127) / 128, N % 4 == 0 && ldy % 4 == 0 && aligned(y, 4 * os),
+                    (ldy * (long long)os) % 16 == 0 && aligned(y, 16)};
   const size_t mats = experts ? (size_t)E : 1;
   const void* in[] = {x, sx, x_rows, counts, w, sw};
   const size_t inb[] = {row_bytes(X, K, ldx, 1), (size_t)X * a.kb * 4, x_rows ? (size_t)M * 4 : 0,

@@ -47,7 +47,7 @@ struct MatmulArgs {
   void* y;
   long long ldy;
   int X, M, N, K, E, kb, nb;   // kb, nb: blocks along K and N
-  bool wide;                   // y's rows take 4-element stores
+  bool wide, wide16;           // y's rows take stores of 4 elements; of 16 bytes
 };
 
 // The tile of y that a workgroup computes: rows [first, first + rows) and
@@ -77,47 +77,43 @@ __device__ __forceinline__ MmTile tile_of_matrix(const MatmulArgs& a, int n_tile
 // gives each expert's first tile and first row.
 template <int BM>
 __device__ __forceinline__ MmTile tile_of_experts(const MatmulArgs& a, int n_tiles, int lane) {
-  int c4[4];
-  auto request = [&](int e0) {
+  // of this lane's experts e0 + 64 i + lane: first row, rows (those beyond M are not computed), tiles, and the tiles up
+  // to their end; rows and tiles of the experts before
+  int r0[4], used[4], n[4], t1[4], tiles = 0, rows = 0;
+  auto scan = [&](int e0) {
+    int c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c4[i] = a.counts[min(e0 + 64 * i + lane, a.E - 1)];
+    for (int i = 0; i < 4; ++i) c[i] = a.counts[min(e0 + 64 * i + lane, a.E - 1)];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c4[i] = e0 + 64 * i + lane < a.E ? min(max(c4[i], 0), a.M) : 0;
+    for (int i = 0; i < 4; ++i) {
+      t1[i] = 0;
+      if (e0 + 64 * i >= a.E) continue;
+      const int v = e0 + 64 * i + lane < a.E ? min(max(c[i], 0), a.M) : 0;
+      const int r1 = rows + wave_incl_scan(v);
+      r0[i] = r1 - v;
+      used[i] = min(r1, a.M) - min(r0[i], a.M);
+      n[i] = (used[i] + BM - 1) / BM;
+      t1[i] = tiles + wave_incl_scan(n[i]);
+      tiles = __builtin_amdgcn_readlane(t1[i], 63);
+      rows = min(__builtin_amdgcn_readlane(r1, 63), a.M);
+    }
   };
-  // rows and tiles of the experts before the current 64
-  int tiles0 = 0, rows0 = 0;
-  // this lane's expert: its first row, its rows (those beyond M are not computed), the tiles up to its end
-  auto scan = [&](int c, int& r0, int& used, int& n, int& t1) {
-    const int r1 = rows0 + wave_incl_scan(c);
-    r0 = r1 - c;
-    used = min(r1, a.M) - min(r0, a.M);
-    n = (used + BM - 1) / BM;
-    t1 = tiles0 + wave_incl_scan(n);
-    tiles0 = __builtin_amdgcn_readlane(t1, 63);
-    rows0 = min(__builtin_amdgcn_readlane(r1, 63), a.M);
-  };
-  int r0, used, n, t1;
-  for (int e0 = 0; e0 < a.E; e0 += 256) {
-    request(e0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) scan(c4[i], r0, used, n, t1);
-  }
-  const int total = tiles0 * n_tiles;
+  for (int e0 = 0; e0 < a.E; e0 += 256) scan(e0);
+  const int total = tiles * n_tiles;
   if ((int)blockIdx.x >= total) return {0, 0, 0, 0};
   const int id = xcd_contiguous_block((int)blockIdx.x, total);
   const int mt = id / n_tiles;
-  tiles0 = rows0 = 0;
+  tiles = rows = 0;
   for (int e0 = 0; e0 < a.E; e0 += 256) {
-    if (a.E > 256) request(e0);
+    if (a.E > 256) scan(e0);   // else it is all still there
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      scan(c4[i], r0, used, n, t1);
-      const uint64_t hit = __builtin_amdgcn_ballot_w64(mt < t1);
+      const uint64_t hit = __builtin_amdgcn_ballot_w64(mt < t1[i]);
       if (hit) {
         const int at = (int)__builtin_ctzll(hit);
-        const int k = mt - (__builtin_amdgcn_readlane(t1, at) - __builtin_amdgcn_readlane(n, at));
-        const int rows = __builtin_amdgcn_readlane(used, at) - k * BM;
-        return {e0 + 64 * i + at, __builtin_amdgcn_readlane(r0, at) + k * BM, min(BM, rows), id - mt * n_tiles};
+        const int k = mt - (__builtin_amdgcn_readlane(t1[i], at) - __builtin_amdgcn_readlane(n[i], at));
+        const int left = __builtin_amdgcn_readlane(used[i], at) - k * BM;
+        return {e0 + 64 * i + at, __builtin_amdgcn_readlane(r0[i], at) + k * BM, min(BM, left), id - mt * n_tiles};
       }
     }
   }
@@ -294,23 +290,53 @@ __device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff,
 
 // A wavefront's MT x NT tiles to y: rows m0 .. of the row tile, columns n0 ..
 // (`inside`: all of the workgroup's columns exist).  A row number outside x
-// makes its row NaN.
+// makes its row NaN.  As they are, a lane's 4 results of a 16-bit type are 8
+// bytes, and a store 16 rows of 32 bytes; by way of LDS, 16 rows at a time, in
+// a space of the wavefront's own, it is whole rows of the wavefront's columns,
+// 16 bytes a lane.  `lds`: kMmStoreBytes<NT> bytes of this wavefront's.
+template <int NT>
+constexpr int kMmStoreBytes = 16 * (32 * NT + 16);   // 16 bytes more a row: rows in different banks
 template <typename O, int MT, int NT>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0,
-                                           bool inside, int m0, int lane) {
-  const bool whole = a.wide && inside;
-  const int n = n0 + 4 * (lane >> 4);
+                                           bool inside, int m0, int lane, uint8_t* lds) {
+  const int lr = lane & 15, lq = lane >> 4;
+  if (sizeof(O) == 2 && inside && a.wide16) {
+    constexpr int kRow = 32 * NT + 16, kPieces = 2 * NT, kRows = 64 / kPieces;   // pieces of 16 bytes in a row; rows of a store
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if (m0 + 16 * j >= rt.rows) break;
+      const int r = min(m0 + 16 * j + lr, rt.rows - 1);
+      const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
+      const float nan = bad ? qnan() : 0.0f;   // v + 0 is v, but for a -0
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
+        store4(reinterpret_cast<O*>(lds + lr * kRow + 32 * i + 8 * lq), v, 4, true);
+      }
+      __builtin_amdgcn_wave_barrier();   // one wavefront's LDS accesses take place in order
+#pragma unroll
+      for (int h = 0; h < 16 / kRows; ++h) {
+        const int row = h * kRows + lane / kPieces, piece = lane % kPieces;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRow + 16 * piece);
+        if (m0 + 16 * j + row < rt.rows)
+          *reinterpret_cast<u32x4*>(static_cast<O*>(a.y) + (long long)(rt.first + m0 + 16 * j + row) * a.ldy + n0 + 8 * piece) = v;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
+  }
+  const int n = n0 + 4 * lq;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    const int r = m0 + 16 * j + (lane & 15);
+    const int r = m0 + 16 * j + lr;
     if (r >= rt.rows) continue;
     const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
-    const float nan = bad ? qnan() : 0.0f;   // v + 0 is v, but for a -0
+    const float nan = bad ? qnan() : 0.0f;
     O* row = static_cast<O*>(a.y) + (long long)(rt.first + r) * a.ldy + n;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
-      if (whole) store4(row + 16 * i, v, 4, true);
+      if (inside && a.wide) store4(row + 16 * i, v, 4, true);
       else store4(row + 16 * i, v, a.N - n - 16 * i, a.wide);
     }
   }
@@ -512,7 +538,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 #pragma unroll
   for (int u = 0; u < kLag; ++u) add(kTiles - kLag + u, (kTiles - kLag + u) % kRing, s_prev);
 
-  store_tile<O, MT, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane);
+  static_assert(kWaves * kMmStoreBytes<NT> <= BN * kMmBlock);
+  __syncthreads();   // every wavefront is done with the operands: their space is the results' now
+  store_tile<O, MT, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
 }
 
 // Tiles of 16 rows: the kernel of decode, where a matrix is read for a handful
