@@ -300,7 +300,7 @@ template <typename O, int MT, int NT>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0,
                                            bool inside, int m0, int lane, uint8_t* lds) {
   const int lr = lane & 15, lq = lane >> 4;
-  if (sizeof(O) == 2 && inside && a.wide16) {
+  if constexpr (sizeof(O) == 2) if (inside && a.wide16) {
     constexpr int kRow = 32 * NT + 16, kPieces = 2 * NT, kRows = 64 / kPieces;   // pieces of 16 bytes in a row; rows of a store
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
@@ -326,6 +326,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
     return;
   }
   const int n = n0 + 4 * lq;
+  const bool whole = inside && a.wide;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int r = m0 + 16 * j + lr;
@@ -336,7 +337,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
-      if (inside && a.wide) store4(row + 16 * i, v, 4, true);
+      if (whole) store4(row + 16 * i, v, 4, true);
       else store4(row + 16 * i, v, a.N - n - 16 * i, a.wide);
     }
   }
