@@ -304,10 +304,10 @@ int moe_decode_conventional_noalloc(const void *x, const int32_t *topk_ids, cons
  * A logit of -inf (an expert ruled out) has probability 0; a valid row of -inf
  * only has p = 0 and logsumexp taken as 0.  +inf and NaN give NaN.  The logits
  * of a token that is not valid may hold anything.  Sums are FP32 over at most
- * a few thousand tokens, then FP64, always in the same order: the same inputs
- * give the same bits.  Elements between the rows (ld > E) are neither read
+ * 32768 tokens, then FP64, always in the same order: the same inputs give the
+ * same bits.  Elements between the rows (ld > E) are neither read
  * nor written.
- * Limits: E <= 1024, k <= 64 and k <= E, G divides T, T * k < 2^31,
+ * Limits: E <= 1024, k <= 64 and k <= E, G divides T, T <= 2^30, T * k < 2^31,
  * G <= 2^19, G * E < 2^26, strides up to 2^30.  `workspace` is device memory of at least
  * moe_decode_balance_workspace() bytes, 256-byte aligned, used until the
  * launches complete (calls that may overlap in time need one each); it need
@@ -338,7 +338,7 @@ int moe_decode_balance_backward(const void *logits, long long ld, int dtype, con
  *           in FP32, not rounded before the quantisation
  *   q       uint8 [M, K] E4M3 codes
  *   scales  fp32 [M, ceil(K / 128)]
- * Limits: M * ceil(K / 128) < 2^30, ldx up to 2^30.  M == 0 is a valid no-op. */
+ * Limits: M * ceil(K / 128) < 2^28, K <= 2^28, ldx up to 2^30.  M == 0 is a valid no-op. */
 #define MOE_QUANT_SWIGLU 1
 #define MOE_QUANT_POW2 2
 int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q, float *scales,
@@ -369,7 +369,8 @@ int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q,
  * through: its row of y is NaN.  Rows of y behind the last expert's are left
  * as they were; negative counts are taken as 0, and rows beyond M are not
  * computed.
- * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts), strides up to 2^30.
+ * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts), M and K <= 2^30, strides
+ * up to 2^30, fewer than 2^22 tiles of y (of 64 x 64 where it has few columns).
  * M == 0 is a valid no-op.
  *
  * Kernel variants (the _ex forms take one; 0 = the built-in choice, the

@@ -12,8 +12,8 @@ using moe_host::overlaps;
 int check_balance(int T, int E, int k, int G) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || G <= 0) return MOE_ERR_SHAPE;
   if (E > moe::kBalMaxExperts || k > moe::kBalMaxK || T % G) return MOE_ERR_SHAPE;
-  if ((long long)T * k >= (1LL << 31)) return MOE_ERR_SHAPE;
-  // a launch holds fewer than 2^32 threads: G * ceil(E / 32) workgroups of 1024, G of 512
+  if (T > moe::kBalMaxTokens || (long long)T * k >= (1LL << 31)) return MOE_ERR_SHAPE;
+  // a launch holds fewer than 2^32 threads: G * ceil(E / 32) workgroups of 1024, G (or T / 32768 and some) of 512
   if (G > (1 << 19) || (long long)G * E >= (1LL << 26)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

@@ -43,13 +43,18 @@ constexpr int kBalTargetParts = 512;  // workgroups of a pass: 2 per CU
 constexpr int kBalAhead = 1;          // rounds of rows that a wavefront has requested
 constexpr int kBalAlone = 256;        // tokens that one workgroup takes without a second launch
 
-// Parts each group's tokens are cut into: enough workgroups for the chip, at
-// least 32 tokens each.
+constexpr int kBalMostTokens = 32768; // tokens of a part: what is added up in FP32
+constexpr int kBalMaxTokens = 1 << 30; // T: token numbers a round past the last one are 32-bit too
+
+// Parts each group's tokens are cut into: enough workgroups for the chip, of
+// at least 32 tokens each and few enough for FP32 sums.
 __host__ __device__ constexpr int balance_parts(int S, int G) {
   if ((long long)S * G <= kBalAlone) return 1;
   const int by_chip = (kBalTargetParts + G - 1) / G;
+  const int by_sums = (S + kBalMostTokens - 1) / kBalMostTokens;
   const int by_work = (S + 31) / 32;
-  return by_chip < by_work ? by_chip : by_work;
+  const int parts = by_chip > by_sums ? by_chip : by_sums;
+  return parts < by_work ? parts : by_work;
 }
 
 __host__ __device__ constexpr int balance_splits(int E) { return (E + kBalSumCols - 1) / kBalSumCols; }

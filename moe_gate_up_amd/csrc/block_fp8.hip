@@ -12,6 +12,8 @@ using moe_host::aligned;
 using moe_host::overlaps;
 
 constexpr long long kMaxStride = 1LL << 30;
+constexpr int kMaxSide = 1 << 30;                   // M and K: indices a tile past them are 32-bit too
+constexpr long long kMaxWorkgroups = 1LL << 22;   // of up to 512 threads: a launch holds fewer than 2^32
 
 size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
@@ -167,7 +169,7 @@ MatmulLaunch matmul_launcher(int& variant, const moe::MatmulArgs& a, int y_dtype
 
 int check_matmul(int X, int M, int N, int K, int E, bool experts) {
   if (M < 0 || N <= 0 || K <= 0 || X < 0 || (experts && E <= 0)) return MOE_ERR_SHAPE;
-  if (K % 16 || (long long)N * K >= (1LL << 31)) return MOE_ERR_SHAPE;
+  if (K % 16 || K > kMaxSide || M > kMaxSide || (long long)N * K >= (1LL << 31)) return MOE_ERR_SHAPE;
   if (experts && (E > moe::kMmMaxExperts || M >= moe::kMmMaxExpertRows)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
@@ -199,7 +201,7 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
     if (overlaps(y, row_bytes(M, N, ldy, os), in[i], inb[i])) return MOE_ERR_ALIAS;
   MatmulLaunch fn = matmul_launcher(variant, a, y_dtype);
   if (!fn) return MOE_ERR_ARG;
-  if (fn(false, nullptr, a, y_dtype) >= (1LL << 22)) return MOE_ERR_SHAPE;   // a launch holds fewer than 2^32 threads
+  if (fn(false, nullptr, a, y_dtype) >= kMaxWorkgroups) return MOE_ERR_SHAPE;
   (void)hipGetLastError();
   fn(true, static_cast<hipStream_t>(stream), a, y_dtype);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
@@ -216,7 +218,7 @@ int moe_decode_quantize_fp8(const void* x, long long ldx, int dtype, uint8_t* q,
   const bool swiglu = flags & MOE_QUANT_SWIGLU;
   if (K > (1 << 28)) return MOE_ERR_SHAPE;
   const int nb = (K + moe::kQuantBlock - 1) / moe::kQuantBlock, cols = swiglu ? 2 * K : K;
-  if ((long long)M * nb >= (1LL << 30)) return MOE_ERR_SHAPE;
+  if ((long long)M * nb >= (1LL << 28)) return MOE_ERR_SHAPE;   // 16 threads each, in a launch of fewer than 2^32
   if (M == 0) return MOE_OK;
   if (!stride_ok(M, cols, ldx)) return MOE_ERR_SHAPE;
   if (!x || !q || !scales) return MOE_ERR_NULL;
@@ -264,8 +266,10 @@ int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int* variant, int* wo
   a.X = M, a.M = M, a.N = N, a.K = K, a.E = E, a.kb = (K + 127) / 128, a.nb = (N + 127) / 128;
   int v = 0;
   MatmulLaunch fn = matmul_launcher(v, a, MOE_BF16);
+  const long long blocks = fn(false, nullptr, a, MOE_BF16);
+  if (blocks >= kMaxWorkgroups) return MOE_ERR_SHAPE;
   *variant = v;
-  *workgroups = (int)fn(false, nullptr, a, MOE_BF16);
+  *workgroups = (int)blocks;
   return MOE_OK;
 }
 

@@ -178,3 +178,24 @@ def test_binding_refuses_cpu_tensors():
         mg.moe_decode_matmul_fp8(f(4, 128, **u8), f(4, 1), f(8, 128, **u8), f(1, 1), f(4, 8))
     with pytest.raises(ValueError):
         mg.moe_decode_matmul_fp8_experts(f(4, 128, **u8), f(4, 1), f(2, **i32), f(2, 8, 128, **u8), f(2, 1, 1), f(4, 8))
+
+
+def test_largest_sizes():
+    """The documented limits hold: beyond them 32-bit indices or a launch's 2^32 threads would not."""
+    most = 2 ** 31 - 1
+    n = ctypes.c_size_t()
+    assert mg.lib().moe_decode_balance_workspace(1 << 30, 1, 1, 1, ctypes.byref(n)) == mg.MOE_OK and n.value > 0
+    for T in ((1 << 30) + 1, most):
+        assert mg.lib().moe_decode_balance_workspace(T, 1, 1, 1, ctypes.byref(n)) == mg.MOE_ERR_SHAPE
+        assert balance(T=T, E=1, k=1, ld=1) == mg.MOE_ERR_SHAPE
+        assert backward(T=T, E=1, k=1, ld=1, ld_d=1) == mg.MOE_ERR_SHAPE
+    for bad in (dict(M=1 << 24), dict(M=1 << 28, K=1, ldx=1), dict(M=most, K=1, ldx=1), dict(M=1, K=most, ldx=most)):
+        assert quantize(**bad) == mg.MOE_ERR_SHAPE, bad
+    for bad in (dict(M=most, N=1, K=16, ldx=16, ldy=1), dict(M=1 << 30, N=1, K=16, ldx=16, ldy=1),
+                dict(M=1, N=1, K=most - 15, ldx=most - 15)):
+        for fn in (matmul, experts):
+            assert fn(**bad) == mg.MOE_ERR_SHAPE, bad
+    assert matmul(M=1, N=1 << 26, K=16, ldx=16, ldy=1 << 26) == mg.MOE_ERR_SHAPE
+    for M, N, K, E in ((most, 1, 16, 0), (1 << 30, 1, 16, 0), (1, 1, most - 15, 0), (1, 1 << 26, 16, 0)):
+        v, g = ctypes.c_int(), ctypes.c_int()
+        assert mg.lib().moe_decode_matmul_fp8_plan(M, N, K, E, ctypes.byref(v), ctypes.byref(g)) == mg.MOE_ERR_SHAPE

@@ -333,3 +333,46 @@ def test_no_tokens(dev):
     mg.moe_decode_balance_backward(e(0, 16, device=dev), out[1], out[2], out[0], e(0, 16, device=dev), 2)
     torch.cuda.synchronize()
     assert all(torch.all(o == 3) for o in out)
+
+
+def test_logits_at_the_lowest_value(dev):
+    """Experts ruled out with the type's lowest value, and rows of nothing else: a uniform row, whose square of the
+    logsumexp passes FP32 and is left to the formula."""
+    for dtype in (torch.float32, torch.bfloat16):
+        logits, ids, _ = inputs(31, 2, 40, 24, 4, dtype, dev, None)
+        low = torch.finfo(dtype).min
+        logits[:, 5] = low
+        logits[3] = low
+        gb, gz = 0.7, 0.0
+        losses, counts, tokens, d = run(logits, ids, None, 2, gb, gz)
+        ref = reference(logits, ids, None, 2, gb, gz)
+        assert torch.equal(counts.cpu().long(), ref[1]) and torch.equal(tokens.cpu().long(), ref[2])
+        assert abs(float(losses[0]) - float(ref[0][0])) <= 1e-5 * float(ref[0][0])
+        assert float(losses[1]) == np.inf
+        bound = 1.2e-5 * ref[4] + torch.finfo(dtype).eps / 2 * (ref[3].abs() + 1.2e-5 * ref[4]) + 1.2e-38
+        assert bool(((d.cpu().double() - ref[3]).abs() <= bound).all())
+        assert bool((d[torch.arange(80, device=dev) != 3, 5] == 0).all())
+
+
+def test_a_long_group(dev):
+    """More than 512 parts of 32768 tokens.  A part's sums of non-negative FP32 terms are at most 32768 / 32 = 1024
+    additions of a lane, 2 between lanes and 8 between wavefronts, each off by 2^-24 at most: 6.2e-5, and the terms
+    4e-6 (z's square twice that)."""
+    T, E, k = (1 << 24) + 40000, 8, 1
+    g = torch.Generator(device=dev).manual_seed(5)
+    logits = torch.randn(T, E, generator=g, device=dev).to(torch.bfloat16)
+    ids = torch.randint(0, E, (T, k), generator=g, device=dev, dtype=torch.int32)
+    losses = torch.zeros(2, device=dev)
+    counts = torch.zeros(1, E, dtype=torch.int32, device=dev)
+    tokens = torch.zeros(2, dtype=torch.int32, device=dev)
+    mg.moe_decode_balance(logits, ids, losses, counts, tokens)
+    share, z = torch.zeros(E, dtype=torch.float64, device=dev), 0.0
+    for i in range(0, T, 1 << 22):
+        l = logits[i:i + (1 << 22)].double()
+        share += torch.softmax(l, 1).sum(0)
+        z += float(torch.logsumexp(l, 1).square().sum())
+    c = torch.bincount(ids.flatten().long(), minlength=E)
+    assert torch.equal(counts[0].long(), c) and tokens.tolist() == [T, T]
+    want = [float(E / T * (c / T * share).sum()), z / T]
+    print(f"a long group: {losses.tolist()} for {want}", flush=True)
+    assert abs(float(losses[0]) - want[0]) <= 7e-5 * want[0] and abs(float(losses[1]) - want[1]) <= 7e-5 * want[1]

@@ -349,3 +349,43 @@ def test_refusals(dev):
     with pytest.raises(mg.MoeDecodeError):   # more rows of y than of x, and no row numbers
         mg.moe_decode_matmul_fp8_experts(x, sx, c, we, swe, z(5, 128, dtype=f))
     mg.moe_decode_matmul_fp8(x[:0], sx[:0], w, sw, y[:0])
+
+
+def test_two_calls_at_once(dev):
+    """A product of one matrix and an experts' one on streams of their own, reading the same rows: the bits of each alone."""
+    E, k, N, K, tokens = 16, 4, 384, 1024, 300
+    g = torch.Generator().manual_seed(8)
+    rows, counts, _ = route(g, tokens, E, k, 0.3)
+    x, sx, w, sw = (t.to(dev) for t in make(9, tokens, N, K, E))
+    rows, counts = rows.to(dev), counts.to(dev)
+    y = [torch.empty(tokens, N, dtype=torch.bfloat16, device=dev), torch.empty(tokens * k, N, dtype=torch.bfloat16, device=dev)]
+    one = lambda out, st: mg.moe_decode_matmul_fp8(x, sx, w[3], sw[3], out, stream=st)   # noqa: E731
+    many = lambda out, st: mg.moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, out, x_rows=rows, stream=st)   # noqa: E731
+    one(y[0], None)
+    many(y[1], None)
+    torch.cuda.synchronize()
+    alone = [t.clone() for t in y]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for t in y:
+            t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            one(y[0], streams[0])
+            many(y[1], streams[1])
+        torch.cuda.synchronize()
+        assert torch.equal(y[0], alone[0]) and torch.equal(y[1], alone[1])
+
+
+def test_overlapping_rows_of_one_tensor(dev):
+    """x and the rows of y as columns of one larger tensor each, with sizes that end inside every tile."""
+    M, N, K = 131, 200, 272
+    x, sx, w, sw = make(21, M, N, K)
+    X, W = values(x, sx, False), values(w, sw, True)
+    big = torch.full((M, 3 * K), 0x7F, dtype=torch.uint8, device=dev)
+    big[:, K:2 * K] = x.to(dev)
+    out = torch.full((M, 3 * N), 5.0, dtype=torch.float16, device=dev)
+    mg.moe_decode_matmul_fp8(big[:, K:2 * K], sx.to(dev), w.to(dev), sw.to(dev), out[:, N:2 * N])
+    torch.cuda.synchronize()
+    check(out[:, N:2 * N], X @ W.t(), X.abs() @ W.abs().t(), K, "columns of a larger tensor")
+    assert torch.all(out[:, :N] == 5.0) and torch.all(out[:, 2 * N:] == 5.0)
