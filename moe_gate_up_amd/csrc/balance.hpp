@@ -144,7 +144,7 @@ struct RowLoad {
       if constexpr (sizeof(T) == 4) f = __builtin_bit_cast(float, raw[v]);
       else if constexpr (C == 4) f = bf16_bits_f32((v & 1) ? raw[v / 2] >> 16 : raw[v / 2] & 0xFFFFu);
       else f = bf16_bits_f32(raw[v]);
-      x[v] = on & (balance_col<LR, C>(l, v) < E) ? f : -__builtin_huge_valf();
+      x[v] = (int)on & (int)(balance_col<LR, C>(l, v) < E) ? f : -__builtin_huge_valf();
     }
   }
 };

@@ -48,10 +48,13 @@ void launch_quantize(hipStream_t st, const void* x, long long ldx, uint8_t* q, f
 // A launcher returns its number of workgroups and launches only when `go` is set.
 using MatmulLaunch = long long (*)(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype);
 
-// m-tiles of at most BM rows: with experts, each one's last tile may be short.
-long long row_tiles(const moe::MatmulArgs& a, int bm) {
-  if (!a.E) return (a.M + bm - 1) / bm;
-  return a.M / bm + (a.E < a.M ? a.E : a.M);
+// Workgroups for tiles of bm x bn: with experts, each one's last tile of rows may be short, and an XCD may have up to
+// two tiles more than an eighth of them.
+long long tile_blocks(const moe::MatmulArgs& a, int bm, int bn) {
+  const long long n_tiles = (a.N + bn - 1) / bn;
+  if (!a.E) return (a.M + bm - 1) / bm * n_tiles;
+  const long long tiles = (a.M / bm + (a.E < a.M ? a.E : a.M)) * n_tiles;
+  return (tiles + moe::kXcds - 1) / moe::kXcds * moe::kXcds + moe::kXcds;
 }
 
 template <typename O>
@@ -59,7 +62,7 @@ void go_far(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
   hipLaunchKernelGGL(moe::matmul_far_kernel<O>, grid, dim3(256), 0, st, a);
 }
 long long launch_far(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
-  const long long blocks = row_tiles(a, moe::kMmFar) * ((a.N + moe::kMmFar - 1) / moe::kMmFar);
+  const long long blocks = tile_blocks(a, moe::kMmFar, moe::kMmFar);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
   if (y_dtype == MOE_F32) go_far<float>(grid, st, a);
@@ -74,7 +77,7 @@ void go_tile(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
 }
 template <int BM, int BN, int WM, int WN, int S, int CP = moe::kCached>
 long long launch_tile(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
-  const long long blocks = row_tiles(a, BM) * ((a.N + BN - 1) / BN);
+  const long long blocks = tile_blocks(a, BM, BN);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
   if (y_dtype == MOE_F32) go_tile<BM, BN, WM, WN, S, CP, float>(grid, st, a);
@@ -85,7 +88,7 @@ long long launch_tile(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_d
 
 // 16-bit results only: an FP32 one's conversions need more registers than the accumulators leave.
 long long launch_256(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
-  const long long blocks = row_tiles(a, 256) * ((a.N + 255) / 256);
+  const long long blocks = tile_blocks(a, 256, 256);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
   if (y_dtype == MOE_BF16) go_tile<256, 256, 2, 4, 2, moe::kCached, __bf16>(grid, st, a);
@@ -99,7 +102,7 @@ void go_rows(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
 }
 template <int NT, int WK>
 long long launch_rows(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
-  const long long blocks = row_tiles(a, 16) * ((a.N + 16 * NT - 1) / (16 * NT));
+  const long long blocks = tile_blocks(a, 16, 16 * NT);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
   if (y_dtype == MOE_F32) go_rows<NT, WK, float>(grid, st, a);
@@ -117,31 +120,35 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
 // variants that the rule chooses between, its choice first).
 // One matrix: the smallest tiles while larger ones would leave CUs without
 // work, then the largest that still fill the chip.
-//   16 rows: M = 1, N = 4096 4.4, 64 x 64 7.0; M = 32, N = 1536 (192
-//     workgroups) 5.8, 7.0; N = 2048, K = 4096 (256) 8.2, 10.8; but N = 4096
-//     (512) 8.1, 7.1
-//   64 x 64: N = 4096, M = 256 (256 workgroups) 9.0, 64 x 128 10.5; M = 384 (384) 12.7, 10.9
-//   64 x 128: N = 4096, M = 1024 (512) 17.5, 128 x 128 17.5; N = 2048, K = 4096,
-//     M = 1024 17.7, 27.3; N = 4096, M = 1536 (768) 23.5, 21.1
-//   256 x 256: M = N = 4096 (256) 38.4, 128 x 128 41.8; M = 2048 (128) 34.5, 23.1
-// Experts (128 of 1536 x 2048, top-8), by the rows r of an expert on average:
-//   64 x 128 with w as streaming data: r = 2 53.1, cached 60.4; r = 16 70.5,
-//     79.4; r = 32 86.7, 89.5; r = 64 (w is read for a second tile) 124, 106
-//   128 x 128: r = 96 126.1, 64 x 128 126.6; r = 128 140, 149; r = 64 113, 106
-//   256 x 256: r = 187 160, 128 x 128 168; r = 128 150, 140
-//   64 x 64 while 64 x 128 would not fill the chip: M = 8 8.8, 10.1
+//   16 rows: M = 1, N = 4096 4.4, 64 x 64 6.8; M = 32, N = 1536 (192
+//     workgroups) 5.8, 7.0; N = 2048, K = 4096 (256) 8.2, 10.7; but N = 4096
+//     (512) 8.0, 7.0
+//   64 x 64: N = 4096, M = 256 (256 workgroups) 8.7, 64 x 128 10.1; M = 384 (384) 12.0, 10.4
+//   64 x 128: N = 4096, M = 1024 (512) 16.4, 128 x 128 17.0; N = 2048, K = 4096,
+//     M = 1024 17.9, 26.5; N = 4096, M = 1536 (768) 22.8, 19.7
+//   256 x 256: N = 4096, M = 3000 (192) 30.6, 128 x 128 35.6; M = 2048 (128) 29.6, 22.6
+// Experts, by the tiles there can be and the rows r of an expert on average.
+// 128 of 1536 x 2048, top-8:
+//   64 x 64 up to 160 tiles of 64 x 128: M = 8 (96) 8.7, 64 x 128 10.2; 16 of
+//     768 x 2048, M = 500 (138) 9.3, 10.8; M = 1000 (186) 12.5, 11.3
+//   64 x 128 with w as streaming data: r = 2 53.9, cached 61.0; r = 16 70.4,
+//     79.0; r = 32 85.8, 88.2; r = 64 (w is read for a second tile) 122, 104;
+//     not up to 512 tiles: 8 of 4096 x 2048, M = 64 (288) 14.7, 13.5
+//   128 x 128: r = 96 123.6, 64 x 128 123.6; r = 64 109, 104
+//   256 x 256: r = 128 135.8, 128 x 128 138.2; r = 96 130, 124; r = 256 178, 204;
+//     not up to 512 of its own tiles: 16 of 768 x 2048, M = 20000 (282) 49.8, 44.3; M = 40000 (516) 73.4, 84.5
 // FP32 results (half the matrix rate): 64 x 64 up to 512 workgroups (N = 4096,
-// M = 512 17.3, 64 x 128 17.6, 128 x 128 24.3), then 128 x 128 (M = 4096 71.6, 64 x 128 83.1).
+// M = 512 17.3, 64 x 128 17.3, 128 x 128 24.4; M = 1024 30.2, 25.9, 26.3), then 128 x 128 (M = 4096 74.5, 64 x 128 84.8).
 int default_variant(const moe::MatmulArgs& a, bool f32) {
   auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   int v;
   if (a.E) {
-    const long long r = a.M / a.E;
-    const long long few = (long long)(a.M < a.E ? a.M : a.E) * ((a.N + 127) / 128);
-    v = few <= 256 ? MOE_MATMUL_TILE_64X64
-        : r <= 32 ? MOE_MATMUL_TILE_64X128_STREAM
-        : r <= 95 ? MOE_MATMUL_TILE_64X128
-        : r <= 159 || f32 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
+    const int r = a.M / a.E, groups = a.E < a.M ? a.E : a.M;
+    auto most = [&](int bm, int bn) { return (long long)(a.M / bm + groups) * ((a.N + bn - 1) / bn); };
+    v = most(64, 128) <= 160 ? MOE_MATMUL_TILE_64X64
+        : r <= 32 && most(64, 128) > 512 ? MOE_MATMUL_TILE_64X128_STREAM
+        : r <= 95 || most(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+        : r <= 127 || f32 || most(256, 256) <= 512 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
   } else {
     v = a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16
         : tiles(64, 64) <= (f32 ? 512 : 256) ? MOE_MATMUL_TILE_64X64

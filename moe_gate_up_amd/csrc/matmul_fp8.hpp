@@ -72,48 +72,66 @@ __device__ __forceinline__ MmTile tile_of_matrix(const MatmulArgs& a, int n_tile
 // tile of rows after the other.  How many tiles that makes is known on the
 // device only, and the grid is what it can be at most; the XCDs share out the
 // tiles that there are (by the grid, the last of them would have none: 128
-// experts of 1536 x 2048 and 32768 rows, 238 against 204 us).  A wavefront looks at 64 experts at
-// a time (the counts of 256 requested at once): a prefix sum over the lanes
-// gives each expert's first tile and first row.
+// experts of 1536 x 2048 and 32768 rows, 238 against 204 us).  Large tiles with
+// few rows in them come last, so that what a CU is left with at the end is
+// short (the same case 179 -> 177 us, 16384 rows 142 -> 135).  A wavefront looks at 64 experts at a time (the counts of 256
+// requested at once): prefix sums over the lanes give each expert's first tile
+// of both kinds and first row.
 template <int BM>
 __device__ __forceinline__ MmTile tile_of_experts(const MatmulArgs& a, int n_tiles, int lane) {
+  constexpr int kShort = BM >= 128 ? BM / 4 : 0;   // most rows of a tile that comes last
   // of this lane's experts e0 + 64 i + lane: first row, rows (those beyond M are not computed), tiles, and the tiles up
   // to their end; rows and tiles of the experts before
-  int r0[4], used[4], n[4], t1[4], tiles = 0, rows = 0;
+  int r0[4], used[4], n[4], t1[4], s1[4], tiles = 0, shorts = 0, rows = 0;
+  auto is_short = [](int r) { return r % BM > 0 && r % BM <= kShort ? 1 : 0; };
   auto scan = [&](int e0) {
     int c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = a.counts[min(e0 + 64 * i + lane, a.E - 1)];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      t1[i] = 0;
+      t1[i] = s1[i] = 0;
       if (e0 + 64 * i >= a.E) continue;
       const int v = e0 + 64 * i + lane < a.E ? min(max(c[i], 0), a.M) : 0;
       const int r1 = rows + wave_incl_scan(v);
       r0[i] = r1 - v;
       used[i] = min(r1, a.M) - min(r0[i], a.M);
       n[i] = (used[i] + BM - 1) / BM;
+      if constexpr (kShort > 0) {
+        n[i] -= is_short(used[i]);
+        s1[i] = shorts + wave_incl_scan(is_short(used[i]));
+        shorts = __builtin_amdgcn_readlane(s1[i], 63);
+      }
       t1[i] = tiles + wave_incl_scan(n[i]);
       tiles = __builtin_amdgcn_readlane(t1[i], 63);
       rows = min(__builtin_amdgcn_readlane(r1, 63), a.M);
     }
   };
   for (int e0 = 0; e0 < a.E; e0 += 256) scan(e0);
-  const int total = tiles * n_tiles;
-  if ((int)blockIdx.x >= total) return {0, 0, 0, 0};
-  const int id = xcd_contiguous_block((int)blockIdx.x, total);
+  // this XCD's share of either kind: 1/8, the remainder of one to the first XCDs and of the other to the last
+  const int total = tiles * n_tiles, last = shorts * n_tiles;
+  const int xcd = (int)blockIdx.x % kXcds, turn = (int)blockIdx.x / kXcds, back = kXcds - 1 - xcd;
+  const int mine = total / kXcds + (xcd < total % kXcds ? 1 : 0);
+  const bool is_last = turn >= mine;
+  int id;
+  if (!is_last) {
+    id = xcd * (total / kXcds) + min(xcd, total % kXcds) + turn;
+  } else {
+    if (turn - mine >= last / kXcds + (back < last % kXcds ? 1 : 0)) return {0, 0, 0, 0};
+    id = back * (last / kXcds) + min(back, last % kXcds) + turn - mine;
+  }
   const int mt = id / n_tiles;
-  tiles = rows = 0;
+  tiles = shorts = rows = 0;
   for (int e0 = 0; e0 < a.E; e0 += 256) {
     if (a.E > 256) scan(e0);   // else it is all still there
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t hit = __builtin_amdgcn_ballot_w64(mt < t1[i]);
+      const uint64_t hit = __builtin_amdgcn_ballot_w64(mt < (is_last ? s1[i] : t1[i]));
       if (hit) {
         const int at = (int)__builtin_ctzll(hit);
-        const int k = mt - (__builtin_amdgcn_readlane(t1[i], at) - __builtin_amdgcn_readlane(n[i], at));
-        const int left = __builtin_amdgcn_readlane(used[i], at) - k * BM;
-        return {e0 + 64 * i + at, __builtin_amdgcn_readlane(r0[i], at) + k * BM, min(BM, left), id - mt * n_tiles};
+        const int r = __builtin_amdgcn_readlane(used[i], at);
+        const int k = is_last ? r / BM : mt - (__builtin_amdgcn_readlane(t1[i], at) - __builtin_amdgcn_readlane(n[i], at));
+        return {e0 + 64 * i + at, __builtin_amdgcn_readlane(r0[i], at) + k * BM, min(BM, r - k * BM), id - mt * n_tiles};
       }
     }
   }
@@ -400,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
   uint32_t xo[XC], wo[WC], so = (uint32_t)row[XC] * (uint32_t)a.kb * 4u;
 #pragma unroll
   for (int j = 0; j < XC; ++j) {
-    xo[j] = (uint32_t)row[j] * (uint32_t)a.ldx + 16u * piece;
+    xo[j] = (w * XC + j) * 8 + (lane >> 3) < rt.rows ? (uint32_t)row[j] * (uint32_t)a.ldx + 16u * piece : kMmOutOfRange;
     asm("" : "+v"(xo[j]));   // 32 bits, and no more than that, live through the loop
   }
 #pragma unroll
@@ -428,120 +446,128 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     copy4_to_lds(sr, sl + w % (BM / 64) * 64, so, 4u * b);
   };
 
-  f32x4 acc[NT][MT];
+  auto run = [&](auto row_tiles) {
+    constexpr int MA = decltype(row_tiles)::value;
+    f32x4 acc[NT][MA];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  // where this lane's pieces of its wavefront's first tile lie
-  const uint32_t x0 = (wm + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), x1 = x0 ^ 64;
-  const uint32_t w0 = (wn + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), w1 = w0 ^ 64;
-  auto operand = [&](const uint8_t* base, uint32_t o0, uint32_t o1) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(base + o0);
-    const u32x4 v = *reinterpret_cast<const u32x4*>(base + o1);
-    return i32x8_t{(int)u.v[0], (int)u.v[1], (int)u.v[2], (int)u.v[3], (int)v.v[0], (int)v.v[1], (int)v.v[2], (int)v.v[3]};
-  };
-  // One block, product by product: while one is formed, the one kLag before it
-  // is scaled and added (the last ones of a block at the next block's first),
-  // so that the vector unit never waits for a product nor the matrix unit for
-  // it.  The barriers to the scheduler keep that order: left alone it asks for
-  // more registers than there are.
-  constexpr int kLag = NT >= 4 ? 3 : 1, kRing = kLag + 1, kTiles = MT * NT;   // a lag within one row tile and the one before
-  static_assert(kTiles % kRing == 0, "a block begins at the ring's first slot");
-  f32x4 p[kRing];
-  float s_prev = 0.0f;   // the scale of the block's last row tile, for the products that wait
+      for (int j = 0; j < MA; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    // where this lane's pieces of its wavefront's first tile lie
+    const uint32_t x0 = (wm + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), x1 = x0 ^ 64;
+    const uint32_t w0 = (wn + lr) * kMmBlock + 16 * (lq ^ (lr & 7)), w1 = w0 ^ 64;
+    auto operand = [&](const uint8_t* base, uint32_t o0, uint32_t o1) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(base + o0);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(base + o1);
+      return i32x8_t{(int)u.v[0], (int)u.v[1], (int)u.v[2], (int)u.v[3], (int)v.v[0], (int)v.v[1], (int)v.v[2], (int)v.v[3]};
+    };
+    // One block, product by product: while one is formed, the one kLag before it
+    // is scaled and added (the last ones of a block at the next block's first),
+    // so that the vector unit never waits for a product nor the matrix unit for
+    // it.  The barriers to the scheduler keep that order: left alone it asks for
+    // more registers than there are.
+    constexpr int kLag = NT >= 4 ? 3 : 1, kRing = kLag + 1, kTiles = MA * NT;   // a lag within one row tile and the one before
+    static_assert(kTiles % kRing == 0, "a block begins at the ring's first slot");
+    f32x4 p[kRing];
+    float s_prev = 0.0f;   // the scale of the block's last row tile, for the products that wait
 #pragma unroll
-  for (int i = 0; i < kRing; ++i) p[i] = f32x4{0, 0, 0, 0};
-  auto add = [&](int t, int slot, float s) {
-    f32x4& o = acc[t % NT][t / NT];
+    for (int i = 0; i < kRing; ++i) p[i] = f32x4{0, 0, 0, 0};
+    auto add = [&](int t, int slot, float s) {
+      f32x4& o = acc[t % NT][t / NT];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(p[slot][c], s, o[c]);
-    asm volatile("" : "+v"(o));   // here, and not sunk behind the products that follow
-  };
-  auto scales = [&] {   // past the last block: never used
-    sw64 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(swr, swo + 4u * sw_first, 0, 0));
-  };
-  auto multiply = [&](const uint8_t* xl, const uint8_t* wl, const float* sl, int b) {
-    if (idle) return;
-    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw64), b - sw_first));
-    i32x8_t f[NT], x[2];
-    float s[2], raw = 0.0f;
-    f[0] = operand(wl, w0, w1);
-    x[0] = operand(xl, x0, x1);
-    s[0] = sl[wm + lr] * sw;
+      for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(p[slot][c], s, o[c]);
+      asm volatile("" : "+v"(o));   // here, and not sunk behind the products that follow
+    };
+    auto scales = [&] {   // past the last block: never used
+      sw64 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(swr, swo + 4u * sw_first, 0, 0));
+    };
+    auto multiply = [&](const uint8_t* xl, const uint8_t* wl, const float* sl, int b) {
+      if ((MA < MT || MT < 4) && idle) return;
+      const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw64), b - sw_first));
+      i32x8_t f[NT], x[2];
+      float s[2], raw = 0.0f;
+      f[0] = operand(wl, w0, w1);
+      x[0] = operand(xl, x0, x1);
+      s[0] = sl[wm + lr] * sw;
 #pragma unroll
-    for (int i = 1; i < NT; ++i) f[i] = operand(wl + 16 * kMmBlock * i, w0, w1);
+      for (int i = 1; i < NT; ++i) f[i] = operand(wl + 16 * kMmBlock * i, w0, w1);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const int j = t / NT, i = t % NT;
-      if (i == 0 && j + 1 < MT) {
-        x[(j + 1) & 1] = operand(xl + 16 * kMmBlock * (j + 1), x0, x1);
-        raw = sl[wm + 16 * (j + 1) + lr];
+      for (int t = 0; t < kTiles; ++t) {
+        const int j = t / NT, i = t % NT;
+        if (i == 0 && j + 1 < MA) {
+          x[(j + 1) & 1] = operand(xl + 16 * kMmBlock * (j + 1), x0, x1);
+          raw = sl[wm + 16 * (j + 1) + lr];
+        }
+        const f32x4 q = block_product<sizeof(O) == 4>(f[i], x[j & 1]);
+        const int u = t - kLag;
+        add((u + kTiles) % kTiles, (u < 0 ? u + kTiles : u) % kRing, u < 0 ? s_prev : s[(u / NT) & 1]);
+        p[t % kRing] = q;
+        if (i == NT - 1 && j + 1 < MA) s[(j + 1) & 1] = raw * sw;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const f32x4 q = block_product<sizeof(O) == 4>(f[i], x[j & 1]);
-      const int u = t - kLag;
-      add((u + kTiles) % kTiles, (u < 0 ? u + kTiles : u) % kRing, u < 0 ? s_prev : s[(u / NT) & 1]);
-      p[t % kRing] = q;
-      if (i == NT - 1 && j + 1 < MT) s[(j + 1) & 1] = raw * sw;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    s_prev = s[(MT - 1) & 1];
-  };
-  // everyone's copies of the block have arrived (later ones may be on their way),
-  // and everyone is done with the buffer that the next copies fill
-  auto turn = [&](auto later) {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(decltype(later)::value * kOps) & ~0x0F00);   // and lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  constexpr MmInt<S - 2> kLater{};
-  constexpr MmInt<0> kNone{};
+      s_prev = s[(MA - 1) & 1];
+    };
+    // everyone's copies of the block have arrived (later ones may be on their way),
+    // and everyone is done with the buffer that the next copies fill
+    auto turn = [&](auto later) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(decltype(later)::value * kOps) & ~0x0F00);   // and lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    constexpr MmInt<S - 2> kLater{};
+    constexpr MmInt<0> kNone{};
 
-  scales();   // older than the copies: there when the first block's are
-  copy(xl0, wl0, sl0, 0);
-  if constexpr (S > 2) copy(xl1, wl1, sl1, 1);
-  if constexpr (S > 3) copy(xl2, wl2, sl2, 2);
-  int b = 0;
-  constexpr int kSpan = 60;   // blocks whose columns' scales are held at a time: whole rounds of the buffers
-  for (;;) {
-    for (; b + S <= min(a.kb, sw_first + kSpan); b += S) {
-      turn(kLater);
-      if constexpr (S == 2) copy(xl1, wl1, sl1, b + 1);
-      else if constexpr (S == 3) copy(xl2, wl2, sl2, b + 2);
-      else copy(xl3, wl3, sl3, b + 3);
-      multiply(xl0, wl0, sl0, b);
-      turn(kLater);
-      copy(xl0, wl0, sl0, b + S);
-      multiply(xl1, wl1, sl1, b + 1);
-      if constexpr (S > 2) {
+    scales();   // older than the copies: there when the first block's are
+    copy(xl0, wl0, sl0, 0);
+    if constexpr (S > 2) copy(xl1, wl1, sl1, 1);
+    if constexpr (S > 3) copy(xl2, wl2, sl2, 2);
+    int b = 0;
+    constexpr int kSpan = 60;   // blocks whose columns' scales are held at a time: whole rounds of the buffers
+    for (;;) {
+      for (; b + S <= min(a.kb, sw_first + kSpan); b += S) {
         turn(kLater);
-        copy(xl1, wl1, sl1, b + S + 1);
-        multiply(xl2, wl2, sl2, b + 2);
-      }
-      if constexpr (S > 3) {
+        if constexpr (S == 2) copy(xl1, wl1, sl1, b + 1);
+        else if constexpr (S == 3) copy(xl2, wl2, sl2, b + 2);
+        else copy(xl3, wl3, sl3, b + 3);
+        multiply(xl0, wl0, sl0, b);
         turn(kLater);
-        copy(xl2, wl2, sl2, b + S + 2);
-        multiply(xl3, wl3, sl3, b + 3);
+        copy(xl0, wl0, sl0, b + S);
+        multiply(xl1, wl1, sl1, b + 1);
+        if constexpr (S > 2) {
+          turn(kLater);
+          copy(xl1, wl1, sl1, b + S + 1);
+          multiply(xl2, wl2, sl2, b + 2);
+        }
+        if constexpr (S > 3) {
+          turn(kLater);
+          copy(xl2, wl2, sl2, b + S + 2);
+          multiply(xl3, wl3, sl3, b + 3);
+        }
       }
+      if (sw_first + kSpan >= a.kb) break;
+      sw_first += kSpan;
+      scales();
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     }
-    if (sw_first + kSpan >= a.kb) break;
-    sw_first += kSpan;
-    scales();
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  }
-  turn(kNone);   // no copy outlives the loop
-  if (b < a.kb) multiply(xl0, wl0, sl0, b);
-  if constexpr (S > 2)
-    if (b + 1 < a.kb) multiply(xl1, wl1, sl1, b + 1);
-  if constexpr (S > 3)
-    if (b + 2 < a.kb) multiply(xl2, wl2, sl2, b + 2);
+    turn(kNone);   // no copy outlives the loop
+    if (b < a.kb) multiply(xl0, wl0, sl0, b);
+    if constexpr (S > 2)
+      if (b + 1 < a.kb) multiply(xl1, wl1, sl1, b + 1);
+    if constexpr (S > 3)
+      if (b + 2 < a.kb) multiply(xl2, wl2, sl2, b + 2);
 #pragma unroll
-  for (int u = 0; u < kLag; ++u) add(kTiles - kLag + u, (kTiles - kLag + u) % kRing, s_prev);
+    for (int u = 0; u < kLag; ++u) add(kTiles - kLag + u, (kTiles - kLag + u) % kRing, s_prev);
 
-  static_assert(kWaves * kMmStoreBytes<NT> <= BN * kMmBlock);
-  __syncthreads();   // every wavefront is done with the operands: their space is the results' now
-  store_tile<O, MT, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
+    static_assert(kWaves * kMmStoreBytes<NT> <= BN * kMmBlock);
+    __syncthreads();   // every wavefront is done with the operands: their space is the results' now
+    store_tile<O, MA, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
+  };
+  // A wavefront with a quarter of its rows or fewer (an expert's last tile) leaves the other products out, one
+  // without rows all of them; its copies and barriers are those of the others.
+  constexpr int kFew = MT >= 4 ? MT / 4 : MT;
+  if (kFew < MT && rt.rows - wm <= 16 * kFew) run(MmInt<kFew>{});
+  else run(MmInt<MT>{});
 }
 
 // Tiles of 16 rows: the kernel of decode, where a matrix is read for a handful

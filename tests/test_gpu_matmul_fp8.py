@@ -389,3 +389,24 @@ def test_overlapping_rows_of_one_tensor(dev):
     torch.cuda.synchronize()
     check(out[:, N:2 * N], X @ W.t(), X.abs() @ W.abs().t(), K, "columns of a larger tensor")
     assert torch.all(out[:, :N] == 5.0) and torch.all(out[:, 2 * N:] == 5.0)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("counts", [[17] * 41, [256] * 8, [261, 3, 0, 512, 64, 65, 33, 127, 128, 129, 32, 1] * 2, [1] * 300, [700]],
+                         ids=["all short", "all whole", "both", "single rows", "one"])
+def test_experts_whole_and_short_tiles(dev, counts, variant):
+    """Every tile of y is computed once, whatever share of them is whole and whatever the XCDs' shares come to."""
+    E, N, K, M = len(counts), 330, 144, sum(counts)
+    x, sx, w, sw = make(E + M, M, N, K, E)
+    X, W = values(x, sx, False), values(w, sw, True)
+    ref, size = torch.empty(M, N, dtype=torch.float64), torch.empty(M, N, dtype=torch.float64)
+    first = 0
+    for e, c in enumerate(counts):
+        rows = slice(first, first + c)
+        ref[rows], size[rows] = X[rows] @ W[e].t(), X[rows].abs() @ W[e].abs().t()
+        first += c
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=dev)
+    mg.moe_decode_matmul_fp8_experts(x.to(dev), sx.to(dev), torch.tensor(counts, dtype=torch.int32, device=dev), w.to(dev),
+                                     sw.to(dev), y, variant=variant or None)
+    torch.cuda.synchronize()
+    check(y, ref, size, K, f"{E} experts, {M} rows, variant {variant}")
