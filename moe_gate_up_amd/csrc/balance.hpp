@@ -19,9 +19,10 @@
 // Backward: the same walk with f_ge in registers; the softmax is computed
 // again rather than stored (a stored one would be T E more bytes each way).
 //
-// 262144 tokens of 128 experts, FP32, 64 padded groups: forward 30 us, of them
-// 8 the second launch, both 89 us for 410 MB (4.6 TB/s; a copy of that size
-// 6.3): memory, and about 120 vector instructions for 4 rows.  More wavefronts
+// 262144 tokens of 128 experts, FP32, 64 padded groups: forward 40 us and 7 for
+// the second launch, backward 41, together 88 us for 410 MB (4.7 TB/s; a copy of
+// that size 6.3): memory, and about 120 vector instructions for 4 rows.  The
+// forward pass alone, with its counting left out, is 1.5 us faster.  More wavefronts
 // (1024 parts: the forward 52 us) or a second round requested ahead (the same)
 // do not help.  4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which
 // is their latency.
@@ -180,8 +181,9 @@ __device__ __forceinline__ A wave_sum(A v) {
   return v;
 }
 
-// One part of group g: blocks of 8 wavefronts' rows, `parts` blocks apart.  ALONE: there is no other (one
-// group, one part), and losses, counts and tokens are written here.
+// One part of group g: blocks of 8 wavefronts' rows, `parts` blocks apart.
+// ALONE: there is no other (one group, one part), and losses, counts and tokens
+// are written here (64 tokens of 128 experts 4.5 us in a graph).
 template <typename T, int LR, int V, int C, bool ALONE>
 __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
     const T* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const uint8_t* __restrict__ valid,
@@ -219,10 +221,9 @@ __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
     if (counted & ((unsigned)e < (unsigned)E)) atomicAdd(&hist[e], 1);
   };
   // Round i of the part: the workgroups' blocks of one round lie side by side,
-  // and the groups begin at different rounds; with a range of its own for
-  // each part all of them read and wrote the same memory channels at a time
-  // (262144 tokens of 128 experts in 64
-  // groups: both passes 96 against 90 us).
+  // and the groups begin at different rounds; with a range of its own for each
+  // part all of them read and wrote the same memory channels at a time (262144
+  // tokens of 128 experts in 64 groups: both passes 96 against 90 us).
   constexpr int kStep = kBalWaves * RW;
   const int rounds = (S + parts * kStep - 1) / (parts * kStep);
   auto token = [&](int i) {
@@ -323,19 +324,6 @@ __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
       npart[blockIdx.x] = n;
     }
   }
-}
-
-// Sum over the workgroup in a fixed order; every thread gets it.
-template <typename A>
-__device__ __forceinline__ A block_sum(A v, A* scratch, int tid) {
-  v = wave_sum(v);
-  if ((tid & 63) == 0) scratch[tid >> 6] = v;
-  __syncthreads();
-  v = scratch[0];
-#pragma unroll
-  for (int i = 1; i < kBalSumWaves; ++i) v += scratch[i];
-  __syncthreads();
-  return v;
 }
 
 // Second launch, one workgroup per (group, COLS experts): adds the parts, writes
@@ -453,16 +441,32 @@ __global__ __launch_bounds__(kBalSumThreads) void balance_sum_kernel(
     z += __hip_atomic_load(&zsum[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     N += m;
   }
-  bal = block_sum(bal, sd, tid);
-  z = block_sum(z, sd, tid);
-  N = block_sum(N, si, tid);
+  bal = wave_sum(bal);
+  z = wave_sum(z);
+  N = wave_sum(N);
+  if ((tid & 63) == 0) {
+    sd[tid >> 6] = bal;
+    sd[kBalSumWaves + (tid >> 6)] = z;
+    si[tid >> 6] = N;
+  }
+  __syncthreads();
   if (tid == 0) {
+#pragma unroll
+    for (int i = 1; i < kBalSumWaves; ++i) {
+      bal += sd[i];
+      z += sd[kBalSumWaves + i];
+      N += si[i];
+    }
     losses[0] = (float)(bal / (double)G);
     losses[1] = N > 0 ? (float)(z / (double)N) : 0.0f;
     tokens[G] = N;
   }
 }
 
+// The gradient of one part's rows: p_e (F_e - sum_j F_j p_j + zc logsumexp), with
+// F and zc the factors that do not change from row to row of a group.  262144
+// tokens of 128 experts, FP32: 41 us, 268 MB (6.5 TB/s, part of the logits coming
+// from the memory-side cache).
 template <typename T, int LR, int V, int C>
 __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
     const T* __restrict__ logits, long long ld, const uint8_t* __restrict__ valid, const int32_t* __restrict__ counts,
@@ -484,11 +488,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
     q.r.load(logits + (base + c) * ld, E, l);
     q.on = gvalid[valid ? c : 0];
   };
-  // Round i of the part: the workgroups' blocks of one round lie side by side,
-  // and the groups begin at different rounds; with a range of its own for
-  // each part all of them read and wrote the same memory channels at a time
-  // (262144 tokens of 128 experts in 64
-  // groups: both passes 96 against 90 us).
+  // rounds as in the forward pass
   constexpr int kStep = kBalWaves * RW;
   const int rounds = (S + parts * kStep - 1) / (parts * kStep);
   auto token = [&](int i) {

@@ -373,6 +373,23 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 // The rows' scales of the block are copied to LDS with it.  The columns' scales
 // are one number a block and wavefront (its columns lie in one block of 128):
 // lane l holds that of block l of the current span.
+//
+// 256 x 256, 8192 rows, N = K = 4096: 135 us, 2040 TFLOP/s (the matrix cores
+// alone, on the same codes and with the same scaling, 3700; with the scaling
+// left out 3950).  A workgroup takes 3580 cycles for a block whose products
+// are 2048 of matrix-core time; the rest is waiting at the barrier and for the
+// copies, with one workgroup a CU (128 KB of LDS).  The clock is part of the
+// bound: it falls to 1.87-1.91 GHz under random codes, where zeros run at 2.36
+// and take 110 us.  Tried and slower: w straight into registers (164 us),
+// barriers every half block with lines requested ahead (143), operands
+// requested two row tiles ahead (137), products added one behind (155), a
+// third buffer for w, for which the rows' scales have to leave LDS for registers
+// (147; a gain for experts only, 172 against 177, and their loads cost small
+// problems 10 to 20 %), v_mfma_f32_32x32x64 (a bare loop of it 3340 TFLOP/s against 3700).
+// 128 x 128 (two workgroups a CU): 165 us on the same case; M = 2048, N = 4096,
+// K = 2048 22.6 us.  64 x 128, 32 rows of 128 experts of 1536 x 2048 (8 of
+// them a row): 53.9 us with w as streaming data (6.7 TB/s of the experts that
+// are used), 61.0 without.
 template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
 __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs a) {
   constexpr int kWaves = WM * WN;
@@ -577,7 +594,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // formed, straight into the registers that the products take them from.  The
 // wavefronts' sums are added in LDS, in their order.  w is read once, as
 // streaming data; the products are the exact ones for every type of y: the
-// matrix cores wait for memory all the same.
+// matrix cores wait for memory all the same.  M = 1, N = 4096, K = 2048: 4.4 us
+// in a graph, 8.4 MB (1.9 TB/s): a launch (1.6 us) and two memory latencies,
+// and the joining; 64 x 64 tiles 6.8.  Not for experts: 32 rows of 128 experts
+// 100 us against the tile kernel's 60, whose copies need no registers.
 template <int NT, int WK, typename O>
 __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
   constexpr int BN = 16 * NT, kTurn = 4;
