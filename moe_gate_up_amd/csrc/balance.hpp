@@ -19,12 +19,11 @@
 // Backward: the same walk with f_ge in registers; the softmax is computed
 // again rather than stored (a stored one would be T E more bytes each way).
 //
-// 262144 tokens of 128 experts, FP32, 64 padded groups: forward 40 us and 7 for
-// the second launch, backward 41, together 88 us for 410 MB (4.7 TB/s; a copy of
-// that size 6.3): memory, and about 120 vector instructions for 4 rows.  The
-// forward pass alone, with its counting left out, is 1.5 us faster.  More wavefronts
-// (1024 parts: the forward 52 us) or a second round requested ahead (the same)
-// do not help.  4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which
+// 262144 tokens of 128 experts, FP32, 64 padded groups: both passes 74 us for
+// 410 MB (5.5 TB/s; a copy of that size 6.3), the forward pass alone 33, of them 7
+// the second launch: memory, and about 120 vector instructions for 4 rows.  With
+// its counting left out the forward pass is 1.5 us faster.  More wavefronts (1024
+// parts: 12 us slower) or a second round requested ahead (the same) do not help.  4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which
 // is their latency.
 #pragma once
 
@@ -468,8 +467,8 @@ __global__ __launch_bounds__(kBalSumThreads) void balance_sum_kernel(
 
 // The gradient of one part's rows: p_e (F_e - sum_j F_j p_j + zc logsumexp), with
 // F and zc the factors that do not change from row to row of a group.  262144
-// tokens of 128 experts, FP32: 41 us, 268 MB (6.5 TB/s, part of the logits coming
-// from the memory-side cache).
+// tokens of 128 experts, FP32: 41 us behind the forward pass, 268 MB (6.5 TB/s,
+// part of the logits coming from the memory-side cache).
 template <typename T, int LR, int V, int C>
 __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
     const T* __restrict__ logits, long long ld, const uint8_t* __restrict__ valid, const int32_t* __restrict__ counts,

@@ -124,9 +124,9 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
 //     workgroups) 5.8, 7.0; N = 2048, K = 4096 (256) 8.2, 10.7; but N = 4096
 //     (512) 8.0, 7.0
 //   64 x 64: N = 4096, M = 256 (256 workgroups) 8.7, 64 x 128 10.1; M = 384 (384) 12.0, 10.4
-//   64 x 128: N = 4096, M = 1024 (512) 16.4, 128 x 128 17.0; N = 2048, K = 4096,
-//     M = 1024 17.9, 26.5; N = 4096, M = 1536 (768) 22.8, 19.7
-//   256 x 256: N = 4096, M = 3000 (192) 30.6, 128 x 128 35.6; M = 2048 (128) 29.6, 22.6
+//   64 x 128: N = 4096, M = 1024 (512) 15.7, 128 x 128 17.3; N = 2048, K = 4096,
+//     M = 1024 16.8, 26.6; N = 4096, M = 1536 (768) 23.4, 19.1
+//   256 x 256: N = 4096, M = 3000 (192) 29.8, 128 x 128 33.7; M = 2048 (128) 28.0, 20.5
 // Experts, by the tiles there can be and the rows r of an expert on average.
 // 128 of 1536 x 2048, top-8:
 //   64 x 64 up to 160 tiles of 64 x 128: M = 8 (96) 8.7, 64 x 128 10.2; 16 of
@@ -134,11 +134,11 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
 //   64 x 128 with w as streaming data: r = 2 53.9, cached 61.0; r = 16 70.4,
 //     79.0; r = 32 85.8, 88.2; r = 64 (w is read for a second tile) 122, 104;
 //     not up to 512 tiles: 8 of 4096 x 2048, M = 64 (288) 14.7, 13.5
-//   128 x 128: r = 96 123.6, 64 x 128 123.6; r = 64 109, 104
-//   256 x 256: r = 128 135.8, 128 x 128 138.2; r = 96 130, 124; r = 256 178, 204;
-//     not up to 512 of its own tiles: 16 of 768 x 2048, M = 20000 (282) 49.8, 44.3; M = 40000 (516) 73.4, 84.5
+//   128 x 128: r = 80 111.5, 64 x 128 114.5; r = 64 105.3, 104.8
+//   256 x 256: r = 128 130.8, 128 x 128 134.8; r = 96 123.8, 119.4; r = 256 175, 200;
+//     not up to 512 of its own tiles: 16 of 768 x 2048, M = 20000 (282) 48.7, 43.1; M = 40000 (516) 67.4, 79.8
 // FP32 results (half the matrix rate): 64 x 64 up to 512 workgroups (N = 4096,
-// M = 512 17.3, 64 x 128 17.3, 128 x 128 24.4; M = 1024 30.2, 25.9, 26.3), then 128 x 128 (M = 4096 74.5, 64 x 128 84.8).
+// M = 512 17.3, 64 x 128 17.3, 128 x 128 24.4; M = 1024 30.2, 25.9, 26.3), then 128 x 128 (M = 4096 72.1, 64 x 128 83.1).
 int default_variant(const moe::MatmulArgs& a, bool f32) {
   auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   int v;
@@ -147,7 +147,7 @@ int default_variant(const moe::MatmulArgs& a, bool f32) {
     auto most = [&](int bm, int bn) { return (long long)(a.M / bm + groups) * ((a.N + bn - 1) / bn); };
     v = most(64, 128) <= 160 ? MOE_MATMUL_TILE_64X64
         : r <= 32 && most(64, 128) > 512 ? MOE_MATMUL_TILE_64X128_STREAM
-        : r <= 95 || most(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+        : r <= 71 || most(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
         : r <= 127 || f32 || most(256, 256) <= 512 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
   } else {
     v = a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16

@@ -35,6 +35,7 @@ constexpr int kMmMaxExpertRows = 1 << 24;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half_t;
+typedef uint32_t u32_quad __attribute__((ext_vector_type(4)));
 
 struct MatmulArgs {
   const uint8_t* x;
@@ -311,10 +312,16 @@ __device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff,
 // makes its row NaN.  As they are, a lane's 4 results of a 16-bit type are 8
 // bytes, and a store 16 rows of 32 bytes; by way of LDS, 16 rows at a time, in
 // a space of the wavefront's own, it is whole rows of the wavefront's columns,
-// 16 bytes a lane.  `lds`: kMmStoreBytes<NT> bytes of this wavefront's.
+// 16 bytes a lane.  STREAM: past the caches, which keep the operands for the
+// tiles to come (8192 rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128
+// experts, both products with the quantisation that reads the first's result
+// between them, 314 -> 295; 64 x 128, M = 1024, N = 4096, K = 2048 16.9 -> 15.7);
+// 64 x 64 tiles and experts of few rows have small results, and gain nothing
+// (the latter 54.0 -> 55.2).
+// `lds`: kMmStoreBytes<NT> bytes of this wavefront's.
 template <int NT>
 constexpr int kMmStoreBytes = 16 * (32 * NT + 16);   // 16 bytes more a row: rows in different banks
-template <typename O, int MT, int NT>
+template <typename O, int MT, int NT, bool STREAM>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0,
                                            bool inside, int m0, int lane, uint8_t* lds) {
   const int lr = lane & 15, lq = lane >> 4;
@@ -336,8 +343,11 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
       for (int h = 0; h < 16 / kRows; ++h) {
         const int row = h * kRows + lane / kPieces, piece = lane % kPieces;
         const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRow + 16 * piece);
-        if (m0 + 16 * j + row < rt.rows)
-          *reinterpret_cast<u32x4*>(static_cast<O*>(a.y) + (long long)(rt.first + m0 + 16 * j + row) * a.ldy + n0 + 8 * piece) = v;
+        if (m0 + 16 * j + row < rt.rows) {
+          O* to = static_cast<O*>(a.y) + (long long)(rt.first + m0 + 16 * j + row) * a.ldy + n0 + 8 * piece;
+          if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32_quad, v), reinterpret_cast<u32_quad*>(to));
+          else *reinterpret_cast<u32x4*>(to) = v;
+        }
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -374,20 +384,21 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 // are one number a block and wavefront (its columns lie in one block of 128):
 // lane l holds that of block l of the current span.
 //
-// 256 x 256, 8192 rows, N = K = 4096: 135 us, 2040 TFLOP/s (the matrix cores
+// 256 x 256, 8192 rows, N = K = 4096: 128 us, 2150 TFLOP/s (the matrix cores
 // alone, on the same codes and with the same scaling, 3700; with the scaling
 // left out 3950).  A workgroup takes 3580 cycles for a block whose products
 // are 2048 of matrix-core time; the rest is waiting at the barrier and for the
 // copies, with one workgroup a CU (128 KB of LDS).  The clock is part of the
 // bound: it falls to 1.87-1.91 GHz under random codes, where zeros run at 2.36
-// and take 110 us.  Tried and slower: w straight into registers (164 us),
-// barriers every half block with lines requested ahead (143), operands
-// requested two row tiles ahead (137), products added one behind (155), a
-// third buffer for w, for which the rows' scales have to leave LDS for registers
-// (147; a gain for experts only, 172 against 177, and their loads cost small
-// problems 10 to 20 %), v_mfma_f32_32x32x64 (a bare loop of it 3340 TFLOP/s against 3700).
-// 128 x 128 (two workgroups a CU): 165 us on the same case; M = 2048, N = 4096,
-// K = 2048 22.6 us.  64 x 128, 32 rows of 128 experts of 1536 x 2048 (8 of
+// and took 110 us when random ones took 137.  Tried and not faster than those
+// 137: w straight into registers (164 us), barriers every half block with lines
+// requested ahead (143), operands requested two row tiles ahead (the same),
+// products added one behind (155), a third buffer for w, for which the rows'
+// scales have to leave LDS for registers (147; a gain for experts only, 172
+// against 177, and their loads cost small problems 10 to 20 %),
+// v_mfma_f32_32x32x64 (a bare loop of it 3340 TFLOP/s against 3700).
+// 128 x 128 (two workgroups a CU): 148 us on the same case; M = 2048, N = 4096,
+// K = 2048 20.5 us.  64 x 128, 32 rows of 128 experts of 1536 x 2048 (8 of
 // them a row): 53.9 us with w as streaming data (6.7 TB/s of the experts that
 // are used), 61.0 without.
 template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
@@ -578,7 +589,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 
     static_assert(kWaves * kMmStoreBytes<NT> <= BN * kMmBlock);
     __syncthreads();   // every wavefront is done with the operands: their space is the results' now
-    store_tile<O, MA, NT>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
+    store_tile<O, MA, NT, BN >= 128 && CP != kStream>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
   };
   // A wavefront with a quarter of its rows or fewer (an expert's last tile) leaves the other products out, one
   // without rows all of them; its copies and barriers are those of the others.
