@@ -23,8 +23,8 @@
 // 410 MB (5.5 TB/s; a copy of that size 6.3), the forward pass alone 33, of them 7
 // the second launch: memory, and about 120 vector instructions for 4 rows.  With
 // its counting left out the forward pass is 1.5 us faster.  More wavefronts (1024
-// parts: 12 us slower) or a second round requested ahead (the same) do not help.  4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which
-// is their latency.
+// parts: 12 us slower) or a second round requested ahead (the same) do not help.
+// 4096 tokens: 4.1, 4.2 and 4.2 us for the three launches, which is their latency.
 #pragma once
 
 #include "prims.hpp"

@@ -9,10 +9,12 @@
 // formula bit for bit: a / 448 and v / s are products with the rounded
 // reciprocal and one correction from the exact residual (two fused
 // multiply-adds), where a general division is ten instructions.  8192 x 4096
-// bf16: 18.4 us, 102 MB (5.5 TB/s; a copy of 50 MB each way 5.9); with SwiGLU
-// 32768 x 768: 22.7 us, 127 MB (5.6 TB/s).  Several blocks for each lane, all
-// requested first, are slower than more wavefronts (one 23.0, two 24.0, four
-// 28.1 us, before the divisions were trimmed).
+// bf16: 16.4 us, 102 MB (6.2 TB/s; a copy of 50 MB each way 5.9); with SwiGLU
+// 32768 x 768: 20.7 us, 127 MB (6.1 TB/s).  The codes go past the caches, which
+// the reads then have to themselves (18.3 and 22.7 us without; reads past the
+// caches as well: 18.7 and 20.7).  Several blocks for each lane, all requested
+// first, are slower than more wavefronts (one 23.0, two 24.0, four 28.1 us,
+// before the divisions were trimmed).
 #pragma once
 
 #include "prims.hpp"
@@ -27,6 +29,7 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kQuantMinScale = 0x1p-126f;
 
 typedef _Float16 f16_t;
+typedef uint32_t code_pair __attribute__((ext_vector_type(2)));
 
 template <typename T>
 __device__ __forceinline__ float elem_f32(T v) {
@@ -147,7 +150,8 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __rest
     for (int j = 0; j < 8; ++j)
       if (j < left) out[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
   } else {
-    if (FORM == kQuantWhole || left > 0) *reinterpret_cast<uint2*>(out) = uint2{lo, hi};
+    if (FORM == kQuantWhole || left > 0)
+      __builtin_nontemporal_store(code_pair{lo, hi}, reinterpret_cast<code_pair*>(out));
   }
   if (l == 0) scales[u] = s;
 }
