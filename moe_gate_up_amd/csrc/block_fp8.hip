@@ -137,8 +137,8 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
 //   128 x 128: r = 80 111.5, 64 x 128 114.5; r = 64 105.3, 104.8
 //   256 x 256: r = 128 130.8, 128 x 128 134.8; r = 96 123.8, 119.4; r = 256 175, 200;
 //     not up to 512 of its own tiles: 16 of 768 x 2048, M = 20000 (282) 48.7, 43.1; M = 40000 (516) 67.4, 79.8
-// FP32 results (half the matrix rate): 64 x 64 up to 512 workgroups (N = 4096,
-// M = 512 17.3, 64 x 128 17.3, 128 x 128 24.4; M = 1024 30.2, 25.9, 26.3), then 128 x 128 (M = 4096 72.1, 64 x 128 83.1).
+// FP32 results, half the matrix rate, choose alike (N = 4096: M = 512 64 x 128 17.1,
+// 64 x 64 18.1; M = 1024 24.6, 128 x 128 24.1), but have no 256 x 256 (128 x 128, M = 4096 68.8, 64 x 128 81.3).
 int default_variant(const moe::MatmulArgs& a, bool f32) {
   auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   int v;
@@ -151,8 +151,8 @@ int default_variant(const moe::MatmulArgs& a, bool f32) {
         : r <= 127 || f32 || most(256, 256) <= 512 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
   } else {
     v = a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16
-        : tiles(64, 64) <= (f32 ? 512 : 256) ? MOE_MATMUL_TILE_64X64
-        : !f32 && tiles(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+        : tiles(64, 64) <= 256 ? MOE_MATMUL_TILE_64X64
+        : tiles(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
         : f32 || tiles(256, 256) < 192 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
   }
   const int bm = v == MOE_MATMUL_TILE_256X256 ? 256 : v == MOE_MATMUL_TILE_128X128 ? 128 : 64;
@@ -198,8 +198,7 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
       !aligned(x_rows, 4) || !aligned(counts, 4))
     return MOE_ERR_ALIGN;
   moe::MatmulArgs a{x, ldx, sx, x_rows, counts, w, sw, y, ldy, X, M, N, K, experts ? E : 0, (K + 127) / 128,
-                    (N + 127) / 128, N % 4 == 0 && ldy % 4 == 0 && aligned(y, 4 * os),
-                    (ldy * (long long)os) % 16 == 0 && aligned(y, 16)};
+                    (N + 127) / 128};
   const size_t mats = experts ? (size_t)E : 1;
   const void* in[] = {x, sx, x_rows, counts, w, sw};
   const size_t inb[] = {row_bytes(X, K, ldx, 1), (size_t)X * a.kb * 4, x_rows ? (size_t)M * 4 : 0,

@@ -35,7 +35,6 @@ constexpr int kMmMaxExpertRows = 1 << 24;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half_t;
-typedef uint32_t u32_quad __attribute__((ext_vector_type(4)));
 
 struct MatmulArgs {
   const uint8_t* x;
@@ -48,7 +47,6 @@ struct MatmulArgs {
   void* y;
   long long ldy;
   int X, M, N, K, E, kb, nb;   // kb, nb: blocks along K and N
-  bool wide, wide16;           // y's rows take stores of 4 elements; of 16 bytes
 };
 
 // The tile of y that a workgroup computes: rows [first, first + rows) and
@@ -167,19 +165,18 @@ __device__ __forceinline__ f32x4 block_product(const i32x8_t& w, const i32x8_t& 
   }
 }
 
+// 4 neighbours of a row of y, as one store whatever the row's alignment (the
+// device takes global accesses at any address).
 template <typename O>
-__device__ __forceinline__ void store4(O* p, const f32x4& v, int left, bool wide) {
-  if (wide && left >= 4) {
-    if constexpr (sizeof(O) == 4) {
-      *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
-    } else {
-      O t[4] = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
-      *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, t);
-    }
+__device__ __forceinline__ void store4(O* p, const f32x4& v, int left) {
+  typedef uint32_t whole __attribute__((ext_vector_type(sizeof(O)), aligned(sizeof(O))));
+  O t[4] = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
+  if (left >= 4) {
+    *reinterpret_cast<whole*>(p) = __builtin_bit_cast(whole, t);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) p[i] = (O)v[i];
+    for (int i = 0; i < 3; ++i)
+      if (i < left) p[i] = t[i];
   }
 }
 
@@ -283,7 +280,7 @@ __global__ __launch_bounds__(256) void matmul_far_kernel(MatmulArgs a) {
       const int n = n0 + 32 * (w >> 1) + 16 * i + 4 * lq;
       f32x4 v = acc[i][j];
       if (bad[j]) v = f32x4{qnan(), qnan(), qnan(), qnan()};
-      store4(row + n, v, a.N - n, a.wide);
+      store4(row + n, v, a.N - n);
     }
   }
 }
@@ -307,66 +304,67 @@ __device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
 }
 
-// A wavefront's MT x NT tiles to y: rows m0 .. of the row tile, columns n0 ..
-// (`inside`: all of the workgroup's columns exist).  A row number outside x
-// makes its row NaN.  As they are, a lane's 4 results of a 16-bit type are 8
-// bytes, and a store 16 rows of 32 bytes; by way of LDS, 16 rows at a time, in
-// a space of the wavefront's own, it is whole rows of the wavefront's columns,
-// 16 bytes a lane.  STREAM: past the caches, which keep the operands for the
-// tiles to come (8192 rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128
-// experts, both products with the quantisation that reads the first's result
-// between them, 314 -> 295; 64 x 128, M = 1024, N = 4096, K = 2048 16.9 -> 15.7);
-// 64 x 64 tiles and experts of few rows have small results, and gain nothing
-// (the latter 54.0 -> 55.2).
+// A wavefront's MT x NT tiles to y: rows m0 .. of the row tile, columns n0 ...
+// A row number outside x makes its row NaN.  As they are, a lane's 4 results of
+// a 16-bit type are 8 bytes, and a store 16 rows of 32 bytes; by way of LDS, 16
+// rows at a time, in a space of the wavefront's own, it is whole rows of the
+// wavefront's columns, 16 bytes a lane, at any alignment (5734 x 3855, K = 1696:
+// 97 -> 66 us against stores of 2 bytes; FP32, 777 x 1003, K = 1040 9.3 -> 7.9).
+// STREAM: past the caches, which keep the operands for the tiles to come (8192
+// rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128 experts, both
+// products with the quantisation that reads the first's result between them, 314
+// -> 295; 64 x 128, M = 1024, N = 4096, K = 2048 16.9 -> 15.7); 64 x 64 tiles and
+// experts of few rows have small results, and gain nothing (the latter 54.0 ->
+// 55.2).
 // `lds`: kMmStoreBytes<NT> bytes of this wavefront's.
 template <int NT>
 constexpr int kMmStoreBytes = 16 * (32 * NT + 16);   // 16 bytes more a row: rows in different banks
+typedef uint32_t u32_quad __attribute__((ext_vector_type(4), aligned(2)));
 template <typename O, int MT, int NT, bool STREAM>
-__device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0,
-                                           bool inside, int m0, int lane, uint8_t* lds) {
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt, const f32x4 (&acc)[NT][MT], int n0, int m0,
+                                           int lane, uint8_t* lds) {
   const int lr = lane & 15, lq = lane >> 4;
-  if constexpr (sizeof(O) == 2) if (inside && a.wide16) {
-    constexpr int kRow = 32 * NT + 16, kPieces = 2 * NT, kRows = 64 / kPieces;   // pieces of 16 bytes in a row; rows of a store
+  constexpr int kRow = 32 * NT + 16, kPieces = 2 * NT, kRows = 64 / kPieces;   // pieces of 16 bytes in a row; rows of a store
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      if (m0 + 16 * j >= rt.rows) break;
-      const int r = min(m0 + 16 * j + lr, rt.rows - 1);
-      const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
-      const float nan = bad ? qnan() : 0.0f;   // v + 0 is v, but for a -0
+  for (int j = 0; j < MT; ++j) {
+    if (m0 + 16 * j >= rt.rows) break;
+    const int r = min(m0 + 16 * j + lr, rt.rows - 1);
+    const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
+    const float nan = bad ? qnan() : 0.0f;   // v + 0 is v, but for a -0
+    if constexpr (sizeof(O) == 2) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
-        store4(reinterpret_cast<O*>(lds + lr * kRow + 32 * i + 8 * lq), v, 4, true);
+        O t[4] = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
+        *reinterpret_cast<uint2*>(lds + lr * kRow + 32 * i + 8 * lq) = __builtin_bit_cast(uint2, t);
       }
       __builtin_amdgcn_wave_barrier();   // one wavefront's LDS accesses take place in order
 #pragma unroll
       for (int h = 0; h < 16 / kRows; ++h) {
-        const int row = h * kRows + lane / kPieces, piece = lane % kPieces;
+        const int row = h * kRows + lane / kPieces, piece = lane % kPieces, left = a.N - n0 - 8 * piece;
         const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * kRow + 16 * piece);
-        if (m0 + 16 * j + row < rt.rows) {
-          O* to = static_cast<O*>(a.y) + (long long)(rt.first + m0 + 16 * j + row) * a.ldy + n0 + 8 * piece;
-          if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32_quad, v), reinterpret_cast<u32_quad*>(to));
-          else *reinterpret_cast<u32x4*>(to) = v;
+        if (m0 + 16 * j + row >= rt.rows) continue;
+        O* to = static_cast<O*>(a.y) + (long long)(rt.first + m0 + 16 * j + row) * a.ldy + n0 + 8 * piece;
+        if (left >= 8) {
+          const u32_quad q{v.v[0], v.v[1], v.v[2], v.v[3]};
+          if constexpr (STREAM) __builtin_nontemporal_store(q, reinterpret_cast<u32_quad*>(to));
+          else *reinterpret_cast<u32_quad*>(to) = q;
+        } else {
+          uint16_t t[8];
+          __builtin_memcpy(t, &v, sizeof(t));
+#pragma unroll
+          for (int i = 0; i < 7; ++i)
+            if (i < left) reinterpret_cast<uint16_t*>(to)[i] = t[i];
         }
       }
       __builtin_amdgcn_wave_barrier();
-    }
-    return;
-  }
-  const int n = n0 + 4 * lq;
-  const bool whole = inside && a.wide;
+    } else {
+      if (m0 + 16 * j + lr >= rt.rows) continue;
+      const int n = n0 + 4 * lq;
+      O* row = static_cast<O*>(a.y) + (long long)(rt.first + r) * a.ldy + n;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int r = m0 + 16 * j + lr;
-    if (r >= rt.rows) continue;
-    const bool bad = a.x_rows && (unsigned)a.x_rows[rt.first + r] >= (unsigned)a.X;
-    const float nan = bad ? qnan() : 0.0f;
-    O* row = static_cast<O*>(a.y) + (long long)(rt.first + r) * a.ldy + n;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const f32x4 v = acc[i][j] + f32x4{nan, nan, nan, nan};
-      if (whole) store4(row + 16 * i, v, 4, true);
-      else store4(row + 16 * i, v, a.N - n - 16 * i, a.wide);
+      for (int i = 0; i < NT; ++i)
+        store4(row + 16 * i, acc[i][j] + f32x4{nan, nan, nan, nan}, a.N - n - 16 * i);
     }
   }
 }
@@ -589,7 +587,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 
     static_assert(kWaves * kMmStoreBytes<NT> <= BN * kMmBlock);
     __syncthreads();   // every wavefront is done with the operands: their space is the results' now
-    store_tile<O, MA, NT, BN >= 128 && CP != kStream>(a, rt, acc, n0 + wn, n0 + BN <= a.N, wm, lane, wl0 + w * kMmStoreBytes<NT>);
+    store_tile<O, MA, NT, BN >= 128 && CP != kStream>(a, rt, acc, n0 + wn, wm, lane, wl0 + w * kMmStoreBytes<NT>);
   };
   // A wavefront with a quarter of its rows or fewer (an expert's last tile) leaves the other products out, one
   // without rows all of them; its copies and barriers are those of the others.
@@ -694,7 +692,7 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
   if (bad) v = f32x4{qnan(), qnan(), qnan(), qnan()};
   if (lr < rt.rows) {
     const int n = n0 + 16 * w + 4 * lq;
-    store4(static_cast<O*>(a.y) + (long long)(rt.first + lr) * a.ldy + n, v, a.N - n, a.wide);
+    store4(static_cast<O*>(a.y) + (long long)(rt.first + lr) * a.ldy + n, v, a.N - n);
   }
 }
 
