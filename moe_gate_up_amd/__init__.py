@@ -45,6 +45,7 @@ MOE_MATMUL_TILE_64X128_STREAM = 4
 MOE_MATMUL_TILE_128X128 = 5
 MOE_MATMUL_TILE_256X256 = 6
 MOE_MATMUL_FAR_ROWS = 7
+MOE_MATMUL_FP8_SUMS = 256
 
 EXPORTS = (
     "moe_decode_gate_up", "moe_decode_down", "moe_decode_gate_up_ex", "moe_decode_down_ex",
@@ -445,9 +446,10 @@ def moe_decode_quantize_fp8(x, q, scales, swiglu=False, pow2=False, stream=None)
     return q, scales
 
 
-def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None):
+def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None, fp8_sums=False):
     """y [M,N] = the product of x [M,K] and w [N,K] (E4M3 codes, uint8) with scales sx [M, ceil(K/128)] and
-    sw [ceil(N/128), ceil(K/128)] (see include/moe_decode.h)."""
+    sw [ceil(N/128), ceil(K/128)]; fp8_sums lets a 16-bit y have the FP8 instruction's sums, faster and less exact
+    (see include/moe_decode.h)."""
     L = _load()
     d = _gpu(x, "x")
     M, K = x.shape
@@ -458,14 +460,14 @@ def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None):
     args = (x.data_ptr(), _rows(x, "x", d, M, K), _flat(sx, "sx", d, M * kb, _f32), _flat(w, "w", d, N * K, _u8),
             _flat(sw, "sw", d, -(-N // 128) * kb, _f32), y.data_ptr(), _rows(y, "y", d, M, N),
             _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), M, N, K)
-    if variant is None:
+    if variant is None and not fp8_sums:
         _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8, d, stream, *args)
     else:
-        _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8_ex, d, stream, *args, int(variant))
+        _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8_ex, d, stream, *args, int(variant or 0) | (MOE_MATMUL_FP8_SUMS if fp8_sums else 0))
     return y
 
 
-def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=None, variant=None):
+def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=None, variant=None, fp8_sums=False):
     """The product of moe_decode_matmul_fp8 for E matrices w [E,N,K] on rows sorted by expert, counts [E] (int32) of
     them each; x_rows [M] (int32): the row of x that each row of y comes from (see include/moe_decode.h)."""
     L = _load()
@@ -479,10 +481,10 @@ def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=N
             None if x_rows is None else _flat(x_rows, "x_rows", d, M, _i32), _flat(counts, "counts", d, E, _i32),
             _flat(w, "w", d, E * N * K, _u8), _flat(sw, "sw", d, E * -(-N // 128) * kb, _f32), y.data_ptr(),
             _rows(y, "y", d, M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), X, M, N, K, E)
-    if variant is None:
+    if variant is None and not fp8_sums:
         _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts, d, stream, *args)
     else:
-        _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts_ex, d, stream, *args, int(variant))
+        _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts_ex, d, stream, *args, int(variant or 0) | (MOE_MATMUL_FP8_SUMS if fp8_sums else 0))
     return y
 
 

@@ -13,7 +13,11 @@ using moe_host::overlaps;
 
 constexpr long long kMaxStride = 1LL << 30;
 constexpr int kMaxSide = 1 << 30;                   // M and K: indices a tile past them are 32-bit too
-constexpr long long kMaxWorkgroups = 1LL << 22;   // of up to 512 threads: a launch holds fewer than 2^32
+
+// A launch holds fewer than 2^32 threads: workgroups of 256 (tiles up to 128 x 128) or up to 512.
+constexpr long long max_workgroups(int variant) {
+  return variant == MOE_MATMUL_ROWS_16 || variant == MOE_MATMUL_TILE_256X256 ? 1LL << 22 : 1LL << 24;
+}
 
 size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
@@ -45,8 +49,17 @@ void launch_quantize(hipStream_t st, const void* x, long long ldx, uint8_t* q, f
 }
 
 // ---------------------------------------------------------------- products
-// A launcher returns its number of workgroups and launches only when `go` is set.
-using MatmulLaunch = long long (*)(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype);
+// A launcher returns its number of workgroups and launches only when `go` is set; `fp8`: sums of the FP8 instruction
+// for a 16-bit y.
+using MatmulLaunch = long long (*)(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool fp8);
+
+// f<O, EXACT>() for the type of y and the sums asked for.
+template <typename F>
+void by_result(int y_dtype, bool fp8, F f) {
+  if (y_dtype == MOE_F32) f.template operator()<float, true>();
+  else if (y_dtype == MOE_BF16) fp8 ? f.template operator()<__bf16, false>() : f.template operator()<__bf16, true>();
+  else fp8 ? f.template operator()<moe::half_t, false>() : f.template operator()<moe::half_t, true>();
+}
 
 // Workgroups for tiles of bm x bn: with experts, each one's last tile of rows may be short, and an XCD may have up to
 // two tiles more than an eighth of them.
@@ -57,42 +70,46 @@ long long tile_blocks(const moe::MatmulArgs& a, int bm, int bn) {
   return (tiles + moe::kXcds - 1) / moe::kXcds * moe::kXcds + moe::kXcds;
 }
 
-template <typename O>
-void go_far(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
-  hipLaunchKernelGGL(moe::matmul_far_kernel<O>, grid, dim3(256), 0, st, a);
-}
-long long launch_far(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+struct GoFar {
+  dim3 grid;
+  hipStream_t st;
+  const moe::MatmulArgs& a;
+  template <typename O, bool EXACT>
+  void operator()() const {
+    hipLaunchKernelGGL((moe::matmul_far_kernel<O, EXACT>), grid, dim3(256), 0, st, a);
+  }
+};
+long long launch_far(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool fp8) {
   const long long blocks = tile_blocks(a, moe::kMmFar, moe::kMmFar);
-  if (!go) return blocks;
-  const dim3 grid((unsigned)blocks);
-  if (y_dtype == MOE_F32) go_far<float>(grid, st, a);
-  else if (y_dtype == MOE_BF16) go_far<__bf16>(grid, st, a);
-  else go_far<moe::half_t>(grid, st, a);
+  if (go) by_result(y_dtype, fp8, GoFar{dim3((unsigned)blocks), st, a});
   return blocks;
 }
 
-template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
-void go_tile(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
-  hipLaunchKernelGGL((moe::matmul_tile_kernel<BM, BN, WM, WN, S, CP, O>), grid, dim3(64 * WM * WN), 0, st, a);
-}
+template <int BM, int BN, int WM, int WN, int S, int CP>
+struct GoTile {
+  dim3 grid;
+  hipStream_t st;
+  const moe::MatmulArgs& a;
+  template <typename O, bool EXACT>
+  void operator()() const {
+    hipLaunchKernelGGL((moe::matmul_tile_kernel<BM, BN, WM, WN, S, CP, O, EXACT>), grid, dim3(64 * WM * WN), 0, st, a);
+  }
+};
 template <int BM, int BN, int WM, int WN, int S, int CP = moe::kCached>
-long long launch_tile(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+long long launch_tile(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool fp8) {
   const long long blocks = tile_blocks(a, BM, BN);
-  if (!go) return blocks;
-  const dim3 grid((unsigned)blocks);
-  if (y_dtype == MOE_F32) go_tile<BM, BN, WM, WN, S, CP, float>(grid, st, a);
-  else if (y_dtype == MOE_BF16) go_tile<BM, BN, WM, WN, S, CP, __bf16>(grid, st, a);
-  else go_tile<BM, BN, WM, WN, S, CP, moe::half_t>(grid, st, a);
+  if (go) by_result(y_dtype, fp8, GoTile<BM, BN, WM, WN, S, CP>{dim3((unsigned)blocks), st, a});
   return blocks;
 }
 
-// 16-bit results only: an FP32 one's conversions need more registers than the accumulators leave.
-long long launch_256(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+// 16-bit results on the FP8 instruction only: FP32 sums' conversions need more registers than the accumulators leave (34
+// spilled; 8192 rows, N = K = 4096 223 us, 128 x 128 229).
+long long launch_256(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool) {
   const long long blocks = tile_blocks(a, 256, 256);
   if (!go) return blocks;
-  const dim3 grid((unsigned)blocks);
-  if (y_dtype == MOE_BF16) go_tile<256, 256, 2, 4, 2, moe::kCached, __bf16>(grid, st, a);
-  else go_tile<256, 256, 2, 4, 2, moe::kCached, moe::half_t>(grid, st, a);
+  const GoTile<256, 256, 2, 4, 2, moe::kCached> f{dim3((unsigned)blocks), st, a};
+  if (y_dtype == MOE_BF16) f.operator()<__bf16, false>();
+  else f.operator()<moe::half_t, false>();
   return blocks;
 }
 
@@ -101,7 +118,7 @@ void go_rows(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
   hipLaunchKernelGGL((moe::matmul_rows_kernel<NT, WK, O>), grid, dim3(64 * WK), 0, st, a);
 }
 template <int NT, int WK>
-long long launch_rows(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype) {
+long long launch_rows(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool) {
   const long long blocks = tile_blocks(a, 16, 16 * NT);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
@@ -116,51 +133,83 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
   return (a.x_rows ? (long long)a.X * a.ldx : (bm - 1) * a.ldx + a.K) <= (long long)moe::kMmOutOfRange;
 }
 
-// The built-in choice, from sweeps on MI355X (us; K = 2048 unless stated; the
-// variants that the rule chooses between, its choice first).
+// The built-in choice, from sweeps on MI355X (us in a graph; K = 2048 unless
+// stated; the variants that the rule chooses between, its choice first).
 // One matrix: the smallest tiles while larger ones would leave CUs without
 // work, then the largest that still fill the chip.
-//   16 rows: M = 1, N = 4096 4.4, 64 x 64 6.8; M = 32, N = 1536 (192
-//     workgroups) 5.8, 7.0; N = 2048, K = 4096 (256) 8.2, 10.7; but N = 4096
-//     (512) 8.0, 7.0
-//   64 x 64: N = 4096, M = 256 (256 workgroups) 8.7, 64 x 128 10.1; M = 384 (384) 12.0, 10.4
-//   64 x 128: N = 4096, M = 1024 (512) 15.7, 128 x 128 17.3; N = 2048, K = 4096,
-//     M = 1024 16.8, 26.6; N = 4096, M = 1536 (768) 23.4, 19.1
-//   256 x 256: N = 4096, M = 3000 (192) 29.8, 128 x 128 33.7; M = 2048 (128) 28.0, 20.5
+//   16 rows: M = 1, N = 4096 4.4, 64 x 64 6.8; M = 32, N = 4096 (512
+//     workgroups) 7.8, 9.8; M = 64, N = 2048, K = 4096 (512) 14.0, 17.1; but M =
+//     48, N = 4096 (768) 10.7, 10.2
+//   64 x 64: N = 4096, M = 256 (256 workgroups) 10.9, 64 x 128 14.4; M = 768
+//     (768) 19.5, 20.9; M = 896 (896) 24.1, 21.1
+//   64 x 128: N = 4096, M = 1024 (512) 21.5, 128 x 128 21.8; M = 1536 (768) 30.6,
+//     31.5; M = 2048 (1024) 41.1, 33.7.  128 x 128 is not the fastest where half of
+//     its columns are empty (M = 65536, K = 4096: N = 16 77.4, 64 x 64 70.8; N = 64 78.7, 76.0)
 // Experts, by the tiles there can be and the rows r of an expert on average.
 // 128 of 1536 x 2048, top-8:
+//   64 x 64 up to 256 tiles of 64 x 128: M = 8 (96) 10.7, 64 x 128 14.0; M = 16
+//     (192) 14.3, 14.7; 8 of 4096 x 2048, M = 8 (256) 13.7, 14.3, M = 64 (288) 16.8, 16.6
+//   64 x 128 with w as streaming data: r = 2 55.9, cached 62.5; r = 16 71.4,
+//     80.6; r = 32 87.4, 89.8; r = 40 (w is read for a second tile) 94.7, 92.8
+//   128 x 128: r = 80 122.1, 64 x 128 122.6; r = 72 119.0, 115.7; r = 256 247,
+//     273; not up to 512 tiles of 64 x 128: 16 of 768 x 2048, M = 2000 (282) 22.6, 16.1
+int default_variant(const moe::MatmulArgs& a) {
+  auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (a.E) {
+    const int r = a.M / a.E;
+    const long long most = (long long)(a.M / 64 + (a.E < a.M ? a.E : a.M)) * ((a.N + 127) / 128);
+    return most <= 256 ? MOE_MATMUL_TILE_64X64
+           : r <= 32 ? MOE_MATMUL_TILE_64X128_STREAM
+           : r <= 79 || most <= 512 ? MOE_MATMUL_TILE_64X128 : MOE_MATMUL_TILE_128X128;
+  }
+  return a.M <= 16 || tiles(16, 16) <= 512 ? MOE_MATMUL_ROWS_16
+         : tiles(64, 64) <= 768 ? MOE_MATMUL_TILE_64X64
+         : tiles(64, 128) <= 768 ? MOE_MATMUL_TILE_64X128 : MOE_MATMUL_TILE_128X128;
+}
+
+// The same with the FP8 instruction's sums: its tiles take half the time, so larger ones pay earlier.
+//   16 rows: M = 32, N = 1536 (192 workgroups) 5.8, 64 x 64 7.0; N = 2048, K =
+//     4096 (256) 8.2, 10.7; but N = 4096 (512) 8.0, 7.0
+//   64 x 64: N = 4096, M = 256 (256) 8.7, 64 x 128 10.1; M = 384 (384) 12.0, 10.4
+//   64 x 128: N = 4096, M = 1024 (512) 15.7, 128 x 128 17.3; N = 2048, K = 4096,
+//     M = 1024 16.8, 26.6; N = 4096, M = 1536 (768) 23.4, 19.1
+//   256 x 256: N = 4096, M = 3000 (192) 29.8, 128 x 128 33.7; M = 2048 (128)
+//     28.0, 20.5.  Not the fastest where its last round is nearly empty (N = K =
+//     4096, M = 4352, 272 tiles, 108 against 97; M = 5120, 320, 108 against 102; M
+//     = 6144, 384, 109 against 112) or its columns are (M = 65536, K = 4096: N =
+//     16 84 against 64 x 64 67; N = 128 88 against 128 x 128 71).
+// Experts:
 //   64 x 64 up to 160 tiles of 64 x 128: M = 8 (96) 8.7, 64 x 128 10.2; 16 of
 //     768 x 2048, M = 500 (138) 9.3, 10.8; M = 1000 (186) 12.5, 11.3
 //   64 x 128 with w as streaming data: r = 2 53.9, cached 61.0; r = 16 70.4,
-//     79.0; r = 32 85.8, 88.2; r = 64 (w is read for a second tile) 122, 104;
-//     not up to 512 tiles: 8 of 4096 x 2048, M = 64 (288) 14.7, 13.5
+//     79.0; r = 32 85.8, 88.2; r = 64 122, 104; not up to 512 tiles: 8 of 4096 x
+//     2048, M = 64 (288) 14.7, 13.5
 //   128 x 128: r = 80 111.5, 64 x 128 114.5; r = 64 105.3, 104.8
 //   256 x 256: r = 128 130.8, 128 x 128 134.8; r = 96 123.8, 119.4; r = 256 175, 200;
 //     not up to 512 of its own tiles: 16 of 768 x 2048, M = 20000 (282) 48.7, 43.1; M = 40000 (516) 67.4, 79.8
-// FP32 results, half the matrix rate, choose alike (N = 4096: M = 512 64 x 128 17.1,
-// 64 x 64 18.1; M = 1024 24.6, 128 x 128 24.1), but have no 256 x 256 (128 x 128, M = 4096 68.8, 64 x 128 81.3).
-int default_variant(const moe::MatmulArgs& a, bool f32) {
+int default_variant_fp8(const moe::MatmulArgs& a) {
   auto tiles = [&](int bm, int bn) { return (long long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  int v;
   if (a.E) {
     const int r = a.M / a.E, groups = a.E < a.M ? a.E : a.M;
     auto most = [&](int bm, int bn) { return (long long)(a.M / bm + groups) * ((a.N + bn - 1) / bn); };
-    v = most(64, 128) <= 160 ? MOE_MATMUL_TILE_64X64
-        : r <= 32 && most(64, 128) > 512 ? MOE_MATMUL_TILE_64X128_STREAM
-        : r <= 71 || most(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
-        : r <= 127 || f32 || most(256, 256) <= 512 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
-  } else {
-    v = a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16
-        : tiles(64, 64) <= 256 ? MOE_MATMUL_TILE_64X64
-        : tiles(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
-        : f32 || tiles(256, 256) < 192 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
+    return most(64, 128) <= 160 ? MOE_MATMUL_TILE_64X64
+           : r <= 32 && most(64, 128) > 512 ? MOE_MATMUL_TILE_64X128_STREAM
+           : r <= 71 || most(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+           : r <= 127 || most(256, 256) <= 512 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
   }
-  const int bm = v == MOE_MATMUL_TILE_256X256 ? 256 : v == MOE_MATMUL_TILE_128X128 ? 128 : 64;
-  return v == MOE_MATMUL_ROWS_16 || tile_allowed(a, bm) ? v : MOE_MATMUL_FAR_ROWS;
+  return a.M <= 16 || tiles(16, 16) <= 256 ? MOE_MATMUL_ROWS_16
+         : tiles(64, 64) <= 256 ? MOE_MATMUL_TILE_64X64
+         : tiles(64, 128) <= 512 ? MOE_MATMUL_TILE_64X128
+         : tiles(256, 256) < 192 ? MOE_MATMUL_TILE_128X128 : MOE_MATMUL_TILE_256X256;
 }
 
-MatmulLaunch matmul_launcher(int& variant, const moe::MatmulArgs& a, int y_dtype) {
-  if (variant == 0) variant = default_variant(a, y_dtype == MOE_F32);
+// `variant` becomes the one that is launched.
+MatmulLaunch matmul_launcher(int& variant, bool fp8, const moe::MatmulArgs& a, int y_dtype) {
+  if (variant == 0) {
+    variant = fp8 && y_dtype != MOE_F32 ? default_variant_fp8(a) : default_variant(a);
+    const int bm = variant == MOE_MATMUL_TILE_256X256 ? 256 : variant == MOE_MATMUL_TILE_128X128 ? 128 : 64;
+    if (variant != MOE_MATMUL_ROWS_16 && !tile_allowed(a, bm)) variant = MOE_MATMUL_FAR_ROWS;
+  }
   switch (variant) {
     // 8 wavefronts along K where each of 4 would take more than 4 turns: K = 4096, M = 1 5.9 against 6.7 us; K = 2048 4.6 against 4.4
     case MOE_MATMUL_ROWS_16: return a.kb > 16 ? launch_rows<1, 8> : launch_rows<1, 4>;
@@ -176,7 +225,7 @@ MatmulLaunch matmul_launcher(int& variant, const moe::MatmulArgs& a, int y_dtype
 
 int check_matmul(int X, int M, int N, int K, int E, bool experts) {
   if (M < 0 || N <= 0 || K <= 0 || X < 0 || (experts && E <= 0)) return MOE_ERR_SHAPE;
-  if (K % 16 || K > kMaxSide || M > kMaxSide || (long long)N * K >= (1LL << 31)) return MOE_ERR_SHAPE;
+  if (K % 16 || K > kMaxSide || M >= kMaxSide || (long long)N * K >= (1LL << 31)) return MOE_ERR_SHAPE;
   if (experts && (E > moe::kMmMaxExperts || M >= moe::kMmMaxExpertRows)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
@@ -205,11 +254,13 @@ int matmul_impl(const uint8_t* x, long long ldx, const float* sx, const int32_t*
                         experts ? (size_t)E * 4 : 0, mats * N * K, mats * a.nb * a.kb * 4};
   for (int i = 0; i < 6; ++i)
     if (overlaps(y, row_bytes(M, N, ldy, os), in[i], inb[i])) return MOE_ERR_ALIAS;
-  MatmulLaunch fn = matmul_launcher(variant, a, y_dtype);
+  const bool fp8 = variant & MOE_MATMUL_FP8_SUMS;
+  variant &= ~MOE_MATMUL_FP8_SUMS;
+  MatmulLaunch fn = matmul_launcher(variant, fp8, a, y_dtype);
   if (!fn) return MOE_ERR_ARG;
-  if (fn(false, nullptr, a, y_dtype) >= kMaxWorkgroups) return MOE_ERR_SHAPE;
+  if (fn(false, nullptr, a, y_dtype, fp8) >= max_workgroups(variant)) return MOE_ERR_SHAPE;
   (void)hipGetLastError();
-  fn(true, static_cast<hipStream_t>(stream), a, y_dtype);
+  fn(true, static_cast<hipStream_t>(stream), a, y_dtype, fp8);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
@@ -271,9 +322,9 @@ int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int* variant, int* wo
   moe::MatmulArgs a{};
   a.X = M, a.M = M, a.N = N, a.K = K, a.E = E, a.kb = (K + 127) / 128, a.nb = (N + 127) / 128;
   int v = 0;
-  MatmulLaunch fn = matmul_launcher(v, a, MOE_BF16);
-  const long long blocks = fn(false, nullptr, a, MOE_BF16);
-  if (blocks >= kMaxWorkgroups) return MOE_ERR_SHAPE;
+  MatmulLaunch fn = matmul_launcher(v, false, a, MOE_BF16);
+  const long long blocks = fn(false, nullptr, a, MOE_BF16, false);
+  if (blocks >= max_workgroups(v)) return MOE_ERR_SHAPE;
   *variant = v;
   *workgroups = (int)blocks;
   return MOE_OK;

@@ -2,18 +2,18 @@
 // definition is at moe_decode_matmul_fp8 in include/moe_decode.h), for one
 // matrix and for the experts' matrices on rows sorted by expert.
 //
-// The matrix-core instruction is v_mfma_f32_16x16x128_f8f6f4: its K of 128 is
-// one scale block, so one instruction forms a 16 x 16 tile's unscaled sum of a
-// block from zero, and four v_fma_f32 per lane scale it into the FP32
-// accumulators.  Inside that instruction (as in every FP8 one of this chip)
-// eight neighbouring products are added together first, aligned to the
-// largest of them and cut off 2^-13 below it (probed on the device): on
-// normally distributed codes a block's sum is off by 1.5e-5 of its root mean
-// square, 1/130 of the half step of a bf16 result and 1/16 of an FP16 one's,
-// and never by more than 7/8 * 2^-10 of the sum of the products' magnitudes.
-// An FP32 result would show it: there the codes are converted to bf16, which
-// is exact, and multiplied by v_mfma_f32_16x16x32_bf16, whose sums are FP32
-// (1e-8 on the same data), at half the rate.
+// A block's unscaled sum of a 16 x 16 tile is formed from zero and scaled into
+// the FP32 accumulators with four v_fma_f32 per lane.  There are two ways to form
+// it.  EXACT: the codes are converted to bf16, which is exact, and multiplied by
+// four v_mfma_f32_16x16x32_bf16, whose sums are FP32.  Else one
+// v_mfma_f32_16x16x128_f8f6f4, whose K of 128 is one scale block, at twice the
+// rate: inside it (as in every FP8 instruction of this chip) eight neighbouring
+// products are added together first, aligned to the largest of them and cut off
+// 2^-13 below it (probed on the device), so that sums are not held in 32 bits.  A
+// block's sum is then off by 1.5e-5 of its root mean square on normally
+// distributed codes, 7e-5 with 1 % of the channels 20 times as large, more where
+// the sum cancels, and never by more than 7/8 * 2^-10 of the sum of the products'
+// magnitudes.  It is what a caller asks for, never what one gets.
 // W is the first operand and X the second: lane l then holds
 // row m = l % 16 of y and four neighbouring columns n = 4 (l / 16) + i, so a
 // tile needs one scale per lane (sx[m] sw, sw being the same for the tile's
@@ -150,7 +150,7 @@ __device__ __forceinline__ mm_bf16x8 codes_to_bf16(int lo, int hi) {
   return __builtin_bit_cast(mm_bf16x8, t);
 }
 
-// One block's unscaled sums of a 16 x 16 tile: exact to FP32, or to what the FP8 instruction keeps.
+// One block's unscaled sums of a 16 x 16 tile: in FP32, or in what the FP8 instruction keeps.
 template <bool EXACT>
 __device__ __forceinline__ f32x4 block_product(const i32x8_t& w, const i32x8_t& x) {
   f32x4 p{0, 0, 0, 0};
@@ -186,7 +186,7 @@ __device__ __forceinline__ void store4(O* p, const f32x4& v, int left) {
 // time; piece p of row r lies at position p ^ (r % 8), so that the 16 rows of
 // one operand read fall into different banks.
 constexpr int kMmFar = 64;
-template <typename O>
+template <typename O, bool EXACT>
 __global__ __launch_bounds__(256) void matmul_far_kernel(MatmulArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][kMmFar * kMmBlock];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void matmul_far_kernel(MatmulArgs a) {
       const float sj = sx[j][b] * s;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const f32x4 p = block_product<sizeof(O) == 4>(f[1][i], f[0][j]);
+        const f32x4 p = block_product<EXACT>(f[1][i], f[0][j]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf(p[c], sj, acc[i][j][c]);
       }
@@ -310,12 +310,12 @@ __device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff,
 // rows at a time, in a space of the wavefront's own, it is whole rows of the
 // wavefront's columns, 16 bytes a lane, at any alignment (5734 x 3855, K = 1696:
 // 97 -> 66 us against stores of 2 bytes; FP32, 777 x 1003, K = 1040 9.3 -> 7.9).
-// STREAM: past the caches, which keep the operands for the tiles to come (8192
-// rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128 experts, both
-// products with the quantisation that reads the first's result between them, 314
-// -> 295; 64 x 128, M = 1024, N = 4096, K = 2048 16.9 -> 15.7); 64 x 64 tiles and
-// experts of few rows have small results, and gain nothing (the latter 54.0 ->
-// 55.2).
+// STREAM: past the caches, which keep the operands for the tiles to come (with
+// FP8 sums 8192 rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128
+// experts, both products with the quantisation that reads the first's result
+// between them, 314 -> 295; 64 x 128, M = 1024, N = 4096, K = 2048 16.9 -> 15.7);
+// 64 x 64 tiles and experts of few rows have small results, and gain nothing (the
+// latter 54.0 -> 55.2).
 // `lds`: kMmStoreBytes<NT> bytes of this wavefront's.
 template <int NT>
 constexpr int kMmStoreBytes = 16 * (32 * NT + 16);   // 16 bytes more a row: rows in different banks
@@ -382,9 +382,13 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 // are one number a block and wavefront (its columns lie in one block of 128):
 // lane l holds that of block l of the current span.
 //
-// 256 x 256, 8192 rows, N = K = 4096: 128 us, 2150 TFLOP/s (the matrix cores
-// alone, on the same codes and with the same scaling, 3700; with the scaling
-// left out 3950).  A workgroup takes 3580 cycles for a block whose products
+// FP32 sums, 128 x 128 (two workgroups a CU), 8192 rows, N = K = 4096: 229 us,
+// 1200 TFLOP/s (a library's bf16 product reaches 1471); a block has 64 matrix
+// instructions of a wavefront beside 128 conversions of codes, made by each of the
+// two wavefronts that share a row or a column.
+// Sums of the FP8 instruction, 256 x 256, the same case: 124 to 136 us (the matrix
+// cores alone, on the same codes and with the same scaling, 3700 TFLOP/s; with the
+// scaling left out 3950).  A workgroup takes 3580 cycles for a block whose products
 // are 2048 of matrix-core time; the rest is waiting at the barrier and for the
 // copies, with one workgroup a CU (128 KB of LDS).  The clock is part of the
 // bound: it falls to 1.87-1.91 GHz under random codes, where zeros run at 2.36
@@ -395,11 +399,9 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 // scales have to leave LDS for registers (147; a gain for experts only, 172
 // against 177, and their loads cost small problems 10 to 20 %),
 // v_mfma_f32_32x32x64 (a bare loop of it 3340 TFLOP/s against 3700).
-// 128 x 128 (two workgroups a CU): 148 us on the same case; M = 2048, N = 4096,
-// K = 2048 20.5 us.  64 x 128, 32 rows of 128 experts of 1536 x 2048 (8 of
-// them a row): 53.9 us with w as streaming data (6.7 TB/s of the experts that
-// are used), 61.0 without.
-template <int BM, int BN, int WM, int WN, int S, int CP, typename O>
+// 64 x 128, 2 rows of each of 128 experts of 1536 x 2048: 55.9 us with w as
+// streaming data (6.4 TB/s of the experts that are used), 62.5 without.
+template <int BM, int BN, int WM, int WN, int S, int CP, typename O, bool EXACT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs a) {
   constexpr int kWaves = WM * WN;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;          // 16 x 16 tiles of one wavefront
@@ -524,7 +526,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
           x[(j + 1) & 1] = operand(xl + 16 * kMmBlock * (j + 1), x0, x1);
           raw = sl[wm + 16 * (j + 1) + lr];
         }
-        const f32x4 q = block_product<sizeof(O) == 4>(f[i], x[j & 1]);
+        const f32x4 q = block_product<EXACT>(f[i], x[j & 1]);
         const int u = t - kLag;
         add((u + kTiles) % kTiles, (u < 0 ? u + kTiles : u) % kRing, u < 0 ? s_prev : s[(u / NT) & 1]);
         p[t % kRing] = q;
@@ -602,8 +604,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // time, all loads of the next turn requested before this one's products are
 // formed, straight into the registers that the products take them from.  The
 // wavefronts' sums are added in LDS, in their order.  w is read once, as
-// streaming data; the products are the exact ones for every type of y: the
-// matrix cores wait for memory all the same.  M = 1, N = 4096, K = 2048: 4.4 us
+// streaming data; the sums are always FP32 ones: the matrix cores wait for memory
+// all the same.  M = 1, N = 4096, K = 2048: 4.4 us
 // in a graph, 8.4 MB (1.9 TB/s): a launch (1.6 us) and two memory latencies,
 // and the joining; 64 x 64 tiles 6.8.  Not for experts: 32 rows of 128 experts
 // 100 us against the tile kernel's 60, whose copies need no registers.

@@ -199,3 +199,37 @@ def test_largest_sizes():
     for M, N, K, E in ((most, 1, 16, 0), (1 << 30, 1, 16, 0), (1, 1, most - 15, 0), (1, 1 << 26, 16, 0)):
         v, g = ctypes.c_int(), ctypes.c_int()
         assert mg.lib().moe_decode_matmul_fp8_plan(M, N, K, E, ctypes.byref(v), ctypes.byref(g)) == mg.MOE_ERR_SHAPE
+
+
+def test_built_in_choice_on_both_sides_of_each_threshold():
+    v = lambda *a: mg.moe_decode_matmul_fp8_plan(*a)[0]   # noqa: E731
+    rows, t64, t128, stream, big = (mg.MOE_MATMUL_ROWS_16, mg.MOE_MATMUL_TILE_64X64, mg.MOE_MATMUL_TILE_64X128,
+                                    mg.MOE_MATMUL_TILE_64X128_STREAM, mg.MOE_MATMUL_TILE_128X128)
+    for size, want in (((16, 1 << 20, 128), rows), ((32, 4096, 2048), rows), ((33, 4096, 2048), t64), ((32, 4112, 2048), t64),
+                       ((768, 4096, 2048), t64), ((769, 4096, 2048), t128), ((49152, 64, 2048), t64), ((49153, 64, 2048), big),
+                       ((1536, 4096, 2048), t128), ((1537, 4096, 2048), big), ((8192, 4096, 4096), big)):
+        assert v(*size) == want, size
+    for size, want in (((21, 1536, 2048, 128), t64), ((22, 1536, 2048, 128), stream), ((256, 1536, 2048, 128), stream),
+                       ((4223, 1536, 2048, 128), stream), ((4224, 1536, 2048, 128), t128), ((10239, 1536, 2048, 128), t128),
+                       ((10240, 1536, 2048, 128), big), ((4416, 768, 2048, 16), t128), ((4480, 768, 2048, 16), big)):
+        assert v(*size) == want, size
+
+
+def test_sums_asked_for_with_the_variant():
+    f = mg.MOE_MATMUL_FP8_SUMS
+    for fn in (matmul, experts):
+        assert fn(variant=f | 99) == mg.MOE_ERR_ARG
+        assert fn(variant=2 * f) == mg.MOE_ERR_ARG
+        assert fn(variant=f | mg.MOE_MATMUL_TILE_256X256, dtype=mg.MOE_F32) == mg.MOE_ERR_ARG
+        for v in (0, f, f | mg.MOE_MATMUL_TILE_64X64, mg.MOE_MATMUL_TILE_256X256):
+            assert fn(variant=v, y=at(2, 16)) == mg.MOE_ERR_ALIAS
+
+
+def test_a_launch_holds_fewer_than_2_to_32_threads():
+    """One column of tiles for up to 2^30 - 1 rows, in workgroups of 256 threads."""
+    for M, N in (((1 << 30) - 1, 1), ((1 << 30) - 1, 128), (1 << 29, 128)):
+        variant, blocks = mg.moe_decode_matmul_fp8_plan(M, N, 16)
+        assert variant == mg.MOE_MATMUL_TILE_128X128 and 256 * blocks < 2 ** 32
+    for M, N in ((1 << 30, 1), ((1 << 30) - 1, 300)):
+        with pytest.raises(mg.MoeDecodeError):
+            mg.moe_decode_matmul_fp8_plan(M, N, 16)
