@@ -335,7 +335,8 @@ int moe_decode_balance_backward(const void *logits, long long ld, int dtype, con
  * values as they would be without it.
  *   x       [M, K] of `dtype` (MOE_F32, MOE_BF16 or MOE_F16), row m at m * ldx elements;
  *           with MOE_QUANT_SWIGLU [M, 2K] and v_c = SiLU(x[m, c]) * x[m, K + c]
- *           in FP32, not rounded before the quantisation
+ *           in FP32 (within 6 * 2^-23 of its value; e^-|x| below 2^-126 counts
+ *           as 0), not rounded before the quantisation
  *   q       uint8 [M, K] E4M3 codes
  *   scales  fp32 [M, ceil(K / 128)]
  * Limits: M * ceil(K / 128) < 2^28, K <= 2^28, ldx up to 2^30.  M == 0 is a valid no-op. */

@@ -10,7 +10,7 @@
 // reciprocal and one correction from the exact residual (two fused
 // multiply-adds), where a general division is ten instructions.  8192 x 4096
 // bf16: 16.4 us, 102 MB (6.2 TB/s; a copy of 50 MB each way 5.9); with SwiGLU
-// 32768 x 768: 20.7 us, 127 MB (6.1 TB/s).  The codes go past the caches, which
+// 32768 x 768: 21.3 us, 127 MB (6.0 TB/s).  The codes go past the caches, which
 // the reads then have to themselves (18.3 and 22.7 us without; reads past the
 // caches as well: 18.7 and 20.7).  Several blocks for each lane, all requested
 // first, are slower than more wavefronts (one 23.0, two 24.0, four 28.1 us,
@@ -75,9 +75,19 @@ __device__ __forceinline__ float divide_by(float a, float b, float reciprocal) {
   return __builtin_fmaf(__builtin_fmaf(-t, b, a), reciprocal, t);
 }
 
-// SiLU as in prims.hpp, with the instruction's reciprocal (1 ulp).
-__device__ __forceinline__ float silu_rcp(float g) {
-  return g == -__builtin_huge_valf() ? -0.0f : g * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+// SiLU(g) = g / (1 + e^-g) as n / (1 + a) with a = e^-|g| and n = g or g a, which
+// cannot overflow (a below FP32's normal numbers counts as 0).  a: 2^t with t =
+// -|g| log2 e rounded, and what the rounding left of the exponent added in first
+// order; the quotient: the instruction's reciprocal (1 ulp) and one correction from
+// the exact residual.  Times up that is within (3.5 + |g| / 43) 2^-23 of the exact
+// value; t as it is and the reciprocal alone, (|g| + 4) 2^-23, took 24.2 us where
+// this takes 26.7 (32768 x 768 in a graph), the reciprocal alone 26.4.
+__device__ __forceinline__ float silu_exact(float g) {
+  const float m = __builtin_fabsf(g), t = m * -1.44269502f, e = __builtin_amdgcn_exp2f(t);
+  const float a = __builtin_fmaf(e, __builtin_fmaf(t, -0.693147182f, -m), e);
+  const float n = g >= 0.0f ? g : g * a, d = 1.0f + a, r = __builtin_amdgcn_rcpf(d), q = n * r;
+  const float v = __builtin_fmaf(__builtin_fmaf(-d, q, n), r, q);
+  return g == -__builtin_huge_valf() ? -0.0f : v;
 }
 
 // Unit u = block u % nb of row u / nb; `magic` is ceil(2^32 / nb).
@@ -98,7 +108,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __rest
     float up[8];
     load8<T, FORM>(row + K, left, up);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = silu_rcp(v[j]) * up[j];
+    for (int j = 0; j < 8; ++j) v[j] = silu_exact(v[j]) * up[j];
   }
   auto magnitude = [](float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; };
   uint32_t a = 0;
