@@ -153,7 +153,12 @@ struct RowLoad {
 // returns the log-sum-exp.  A row of -inf only: all three are 0.  A NaN or +inf
 // anywhere makes every probability and the log-sum-exp NaN.  The sum lies in
 // [1, E], so the instructions' reciprocal and logarithm (1 ulp) need no care
-// for range.
+// for range.  A probability is within (|x - max| + 3) 2^-23 of itself, for the
+// rounded product with log2 e and the reciprocal.  With the rounding's rest added
+// and the reciprocal corrected (4096 tokens, FP32, against 64 bits) the losses were
+// as far off as without (2.0e-8 and 2.8e-8 for two inputs), the gradient 8.9e-8 of
+// its norm instead of 9.3e-8 (formed of FP32 torch operations 8.4e-8), and 65536
+// tokens in bf16 took 26.3 us instead of 24.8.
 template <int LR, int V>
 __device__ __forceinline__ float row_softmax(float (&x)[V], float& inv) {
   float m = x[0];
