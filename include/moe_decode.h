@@ -361,7 +361,12 @@ int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q,
  * moe_decode_matmul_fp8_experts: the same for E matrices w [E, N, K], sw [E,
  * ceil(N / 128), ceil(K / 128)] on rows sorted by expert: the first counts[0]
  * rows of y belong to expert 0, the next counts[1] to expert 1, and so on
- * (counts int32 [E], device memory: moe_decode_balance's with G = 1).  Row m
+ * (counts int32 [E], device memory).  moe_decode_balance's counts are those of
+ * its valid tokens' slots with ids in [0, E), group by group: with G = 1, or its
+ * groups' added up, they go with those slots sorted by expert and the slots of
+ * tokens that are not valid, or of other ids, behind them all, where they are not
+ * computed.  (Slots of padding sorted in among the others would shift every later
+ * expert's rows.)  Row m
  * of y comes from row m of x, or from row x_rows[m] where x_rows (int32 [M])
  * is given; x and sx have X rows.  A row number outside [0, X) is not read
  * through: its row of y is NaN.  Rows of y behind the last expert's are left

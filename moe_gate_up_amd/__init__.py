@@ -469,7 +469,10 @@ def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None, fp8_sums=F
 
 def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=None, variant=None, fp8_sums=False):
     """The product of moe_decode_matmul_fp8 for E matrices w [E,N,K] on rows sorted by expert, counts [E] (int32) of
-    them each; x_rows [M] (int32): the row of x that each row of y comes from (see include/moe_decode.h)."""
+    them each; x_rows [M] (int32): the row of x that each row of y comes from (see include/moe_decode.h).
+
+    With moe_decode_balance's counts, added up over its groups, the sorted rows are the slots of valid tokens with ids in
+    [0, E); all other slots go behind them."""
     L = _load()
     d = _gpu(x, "x")
     X, K = x.shape
