@@ -349,14 +349,15 @@ def _rows(t, name, device, rows, cols):
     return ld
 
 
-def _flat(t, name, device, numel, dtype):
-    """Address of a contiguous GPU tensor of that many elements."""
+def _flat(t, name, device, size, dtype):
+    """Address of a contiguous GPU tensor of that shape (a tuple), or of that many elements (a number) where its rows
+    have one meaning only."""
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
     if t.dtype is not dtype and (dtype is not _flags or t.dtype not in _flags):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {numel} contiguous elements, got shape {tuple(t.shape)}, strides {t.stride()}")
+    if (t.numel() if isinstance(size, int) else t.shape) != size or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {size} contiguous elements, got shape {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
 
@@ -409,7 +410,7 @@ def moe_decode_balance(logits, topk_ids, losses, counts, tokens, valid=None, wor
         workspace = _torch.empty(n, dtype=_u8, device=logits.device)
     _call("moe_decode_balance", L.moe_decode_balance, d, stream, logits.data_ptr(), ld, dt,
           _flat(topk_ids, "topk_ids", d, T * k, _i32), None if valid is None else _flat(valid, "valid", d, T, _flags),
-          _flat(losses, "losses", d, 2, _f32), _flat(counts, "counts", d, G * E, _i32),
+          _flat(losses, "losses", d, 2, _f32), _flat(counts, "counts", d, (G, E), _i32),
           _flat(tokens, "tokens", d, G + 1, _i32),
           None if workspace is None else _flat(workspace, "workspace", d, n, _u8), n, T, E, k, G)
     return losses, counts, tokens
@@ -427,7 +428,7 @@ def moe_decode_balance_backward(logits, counts, tokens, grad_losses, dlogits, k,
         raise ValueError("dlogits must have the type of logits")
     _call("moe_decode_balance_backward", L.moe_decode_balance_backward, d, stream, logits.data_ptr(),
           _rows(logits, "logits", d, T, E), dt, None if valid is None else _flat(valid, "valid", d, T, _flags),
-          _flat(counts, "counts", d, G * E, _i32), _flat(tokens, "tokens", d, G + 1, _i32),
+          _flat(counts, "counts", d, (G, E), _i32), _flat(tokens, "tokens", d, G + 1, _i32),
           _flat(grad_losses, "grad_losses", d, 2, _f32), dlogits.data_ptr(), _rows(dlogits, "dlogits", d, T, E),
           T, E, k, G)
     return dlogits
@@ -441,7 +442,7 @@ def moe_decode_quantize_fp8(x, q, scales, swiglu=False, pow2=False, stream=None)
     M, K = q.shape
     _call("moe_decode_quantize_fp8", L.moe_decode_quantize_fp8, d, stream, x.data_ptr(),
           _rows(x, "x", d, M, 2 * K if swiglu else K), _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16)),
-          _flat(q, "q", d, M * K, _u8), _flat(scales, "scales", d, M * -(-K // 128), _f32), M, K,
+          _flat(q, "q", d, M * K, _u8), _flat(scales, "scales", d, (M, -(-K // 128)), _f32), M, K,
           (MOE_QUANT_SWIGLU if swiglu else 0) | (MOE_QUANT_POW2 if pow2 else 0))
     return q, scales
 
@@ -457,8 +458,8 @@ def moe_decode_matmul_fp8(x, sx, w, sw, y, stream=None, variant=None, fp8_sums=F
     kb = -(-K // 128)
     if x.dtype is not _u8:
         raise ValueError(f"x has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
-    args = (x.data_ptr(), _rows(x, "x", d, M, K), _flat(sx, "sx", d, M * kb, _f32), _flat(w, "w", d, N * K, _u8),
-            _flat(sw, "sw", d, -(-N // 128) * kb, _f32), y.data_ptr(), _rows(y, "y", d, M, N),
+    args = (x.data_ptr(), _rows(x, "x", d, M, K), _flat(sx, "sx", d, (M, kb), _f32), _flat(w, "w", d, (N, K), _u8),
+            _flat(sw, "sw", d, (-(-N // 128), kb), _f32), y.data_ptr(), _rows(y, "y", d, M, N),
             _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), M, N, K)
     if variant is None and not fp8_sums:
         _call("moe_decode_matmul_fp8", L.moe_decode_matmul_fp8, d, stream, *args)
@@ -480,9 +481,10 @@ def moe_decode_matmul_fp8_experts(x, sx, counts, w, sw, y, x_rows=None, stream=N
     kb = -(-K // 128)
     if x.dtype is not _u8:
         raise ValueError(f"x has dtype {x.dtype}, expected torch.uint8 (E4M3 codes)")
-    args = (x.data_ptr(), _rows(x, "x", d, X, K), _flat(sx, "sx", d, X * kb, _f32),
-            None if x_rows is None else _flat(x_rows, "x_rows", d, M, _i32), _flat(counts, "counts", d, E, _i32),
-            _flat(w, "w", d, E * N * K, _u8), _flat(sw, "sw", d, E * -(-N // 128) * kb, _f32), y.data_ptr(),
+    args = (x.data_ptr(), _rows(x, "x", d, X, K), _flat(sx, "sx", d, (X, kb), _f32),
+            None if x_rows is None else _flat(x_rows, "x_rows", d, M, _i32),
+            _flat(counts, "counts", d, (E,) if counts.dim() == 1 else (1, E), _i32),
+            _flat(w, "w", d, (E, N, K), _u8), _flat(sw, "sw", d, (E, -(-N // 128), kb), _f32), y.data_ptr(),
             _rows(y, "y", d, M, N), _dtype_code(y, "y", (MOE_F32, MOE_BF16, MOE_F16)), X, M, N, K, E)
     if variant is None and not fp8_sums:
         _call("moe_decode_matmul_fp8_experts", L.moe_decode_matmul_fp8_experts, d, stream, *args)

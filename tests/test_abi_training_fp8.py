@@ -233,3 +233,43 @@ def test_a_launch_holds_fewer_than_2_to_32_threads():
     for M, N in ((1 << 30, 1), ((1 << 30) - 1, 300)):
         with pytest.raises(mg.MoeDecodeError):
             mg.moe_decode_matmul_fp8_plan(M, N, 16)
+
+
+def test_binding_refuses_other_orders_of_the_same_elements(monkeypatch):
+    """Scales block by block instead of row by row, transposed or regrouped matrices, counts expert by expert: as many
+    elements in another order.  (CPU tensors stand in: every call is refused before it reaches the library.)"""
+    import torch
+    mg._load()
+    monkeypatch.setattr(mg, "_gpu", lambda t, name: t.get_device())
+    monkeypatch.setattr(mg, "_call", lambda where, fn, device, stream, *args: pytest.fail(f"{where} was called"))
+    f, u8, i32 = torch.zeros, dict(dtype=torch.uint8), dict(dtype=torch.int32)
+    x, sx, w, sw, y = f(4, 384, **u8), f(4, 3), f(256, 384, **u8), f(2, 3), f(4, 256)
+    ok = [x, sx, w, sw, y]
+    for i, bad in ((1, f(3, 4)), (1, f(12)), (2, f(384, 256, **u8)), (2, f(256, 3, 128, **u8)), (3, f(3, 2)), (3, f(6))):
+        with pytest.raises(ValueError):
+            mg.moe_decode_matmul_fp8(*ok[:i], bad, *ok[i + 1:])
+    ok = [x, sx, f(2, **i32), f(2, 256, 384, **u8), f(2, 2, 3), y]
+    for i, bad in ((1, f(3, 4)), (2, f(2, 1, **i32)), (3, f(2, 256, 3, 128, **u8)), (4, f(2, 3, 2)), (4, f(4, 3)), (4, f(2, 6))):
+        with pytest.raises(ValueError):
+            mg.moe_decode_matmul_fp8_experts(*ok[:i], bad, *ok[i + 1:])
+    with pytest.raises(ValueError):
+        mg.moe_decode_quantize_fp8(f(4, 384), f(4, 384, **u8), f(3, 4))
+    with pytest.raises(ValueError):
+        mg.moe_decode_balance(f(6, 8), f(6, 2, **i32), f(2), f(2, 2, 4, **i32), f(3, **i32))
+    with pytest.raises(ValueError):
+        mg.moe_decode_balance_backward(f(6, 8), f(2, 2, 4, **i32), f(3, **i32), f(2), f(6, 8), 2)
+
+
+def test_binding_takes_what_has_one_meaning(monkeypatch):
+    """A mask by group, ids by group and token, counts of one group as a row."""
+    import torch
+    mg._load()
+    calls = []
+    monkeypatch.setattr(mg, "_gpu", lambda t, name: t.get_device())
+    monkeypatch.setattr(mg, "_call", lambda where, fn, device, stream, *args: calls.append(where))
+    f, u8, i32 = torch.zeros, dict(dtype=torch.uint8), dict(dtype=torch.int32)
+    mg.moe_decode_balance(f(6, 8), f(2, 3, 2, **i32), f(2), f(2, 8, **i32), f(3, **i32), valid=f(2, 3, dtype=torch.bool))
+    for counts in (f(2, **i32), f(1, 2, **i32)):
+        mg.moe_decode_matmul_fp8_experts(f(4, 384, **u8), f(4, 3), counts, f(2, 256, 384, **u8), f(2, 2, 3), f(4, 256),
+                                         x_rows=f(2, 2, **i32))
+    assert len(calls) == 3
