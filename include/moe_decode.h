@@ -339,7 +339,7 @@ int moe_decode_balance_backward(const void *logits, long long ld, int dtype, con
  *           as 0), not rounded before the quantisation
  *   q       uint8 [M, K] E4M3 codes
  *   scales  fp32 [M, ceil(K / 128)]
- * Limits: M * ceil(K / 128) < 2^28, K <= 2^28, ldx up to 2^30.  M == 0 is a valid no-op. */
+ * Limits: M * ceil(K / 128) <= 2^28 - 16, K <= 2^28, ldx up to 2^30.  M == 0 is a valid no-op. */
 #define MOE_QUANT_SWIGLU 1
 #define MOE_QUANT_POW2 2
 int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q, float *scales,

@@ -275,7 +275,8 @@ int moe_decode_quantize_fp8(const void* x, long long ldx, int dtype, uint8_t* q,
   const bool swiglu = flags & MOE_QUANT_SWIGLU;
   if (K > (1 << 28)) return MOE_ERR_SHAPE;
   const int nb = (K + moe::kQuantBlock - 1) / moe::kQuantBlock, cols = swiglu ? 2 * K : K;
-  if ((long long)M * nb >= (1LL << 28)) return MOE_ERR_SHAPE;   // 16 threads each, in a launch of fewer than 2^32
+  // 16 threads each, in workgroups of 256 and a launch of fewer than 2^32
+  if ((long long)M * nb > (1LL << 28) - moe::kQuantThreads / moe::kQuantLanes) return MOE_ERR_SHAPE;
   if (M == 0) return MOE_OK;
   if (!stride_ok(M, cols, ldx)) return MOE_ERR_SHAPE;
   if (!x || !q || !scales) return MOE_ERR_NULL;

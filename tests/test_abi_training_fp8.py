@@ -273,3 +273,11 @@ def test_binding_takes_what_has_one_meaning(monkeypatch):
         mg.moe_decode_matmul_fp8_experts(f(4, 384, **u8), f(4, 3), counts, f(2, 256, 384, **u8), f(2, 2, 3), f(4, 256),
                                          x_rows=f(2, 2, **i32))
     assert len(calls) == 3
+
+
+def test_quantising_launches_fewer_than_2_to_32_threads():
+    """16 threads a block of 128, in workgroups of 256: 2^28 - 16 blocks are the most.  (One more argument is wrong in the
+    calls that the sizes allow, so nothing is launched.)"""
+    for M, K, want in (((1 << 28) - 16, 1, mg.MOE_ERR_ALIAS), ((1 << 28) - 15, 1, mg.MOE_ERR_SHAPE), ((1 << 28) - 1, 128, mg.MOE_ERR_SHAPE),
+                       ((1 << 27) - 8, 129, mg.MOE_ERR_ALIAS), ((1 << 27) - 7, 129, mg.MOE_ERR_SHAPE)):
+        assert quantize(M=M, K=K, ldx=K, q=at(0)) == want, (M, K)
