@@ -113,18 +113,18 @@ long long launch_256(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dt
   return blocks;
 }
 
-template <int NT, int WK, typename O>
+template <int WK, typename O>
 void go_rows(dim3 grid, hipStream_t st, const moe::MatmulArgs& a) {
-  hipLaunchKernelGGL((moe::matmul_rows_kernel<NT, WK, O>), grid, dim3(64 * WK), 0, st, a);
+  hipLaunchKernelGGL((moe::matmul_rows_kernel<WK, O>), grid, dim3(64 * WK), 0, st, a);
 }
-template <int NT, int WK>
+template <int WK>
 long long launch_rows(bool go, hipStream_t st, const moe::MatmulArgs& a, int y_dtype, bool) {
-  const long long blocks = tile_blocks(a, 16, 16 * NT);
+  const long long blocks = tile_blocks(a, 16, 16);
   if (!go) return blocks;
   const dim3 grid((unsigned)blocks);
-  if (y_dtype == MOE_F32) go_rows<NT, WK, float>(grid, st, a);
-  else if (y_dtype == MOE_BF16) go_rows<NT, WK, __bf16>(grid, st, a);
-  else go_rows<NT, WK, moe::half_t>(grid, st, a);
+  if (y_dtype == MOE_F32) go_rows<WK, float>(grid, st, a);
+  else if (y_dtype == MOE_BF16) go_rows<WK, __bf16>(grid, st, a);
+  else go_rows<WK, moe::half_t>(grid, st, a);
   return blocks;
 }
 
@@ -212,7 +212,7 @@ MatmulLaunch matmul_launcher(int& variant, bool fp8, const moe::MatmulArgs& a, i
   }
   switch (variant) {
     // 8 wavefronts along K where each of 4 would take more than 4 turns: K = 4096, M = 1 5.9 against 6.7 us; K = 2048 4.6 against 4.4
-    case MOE_MATMUL_ROWS_16: return a.kb > 16 ? launch_rows<1, 8> : launch_rows<1, 4>;
+    case MOE_MATMUL_ROWS_16: return a.kb > 16 ? launch_rows<8> : launch_rows<4>;
     case MOE_MATMUL_TILE_64X64: return tile_allowed(a, 64) ? launch_tile<64, 64, 2, 2, 3> : nullptr;
     case MOE_MATMUL_TILE_64X128: return tile_allowed(a, 64) ? launch_tile<64, 128, 2, 2, 3> : nullptr;
     case MOE_MATMUL_TILE_64X128_STREAM: return tile_allowed(a, 64) ? launch_tile<64, 128, 2, 2, 3, moe::kStream> : nullptr;

@@ -408,12 +408,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
   constexpr int XC = BM / 8 / kWaves, WC = BN / 8 / kWaves;    // copies (8 rows each) of one wavefront
   constexpr int kOps = XC + WC + 1;                            // copies of one block, with the scales
   static_assert(BN / WN <= kMmBlock && kMmBlock % (BN / WN) == 0 && XC * 8 * kWaves == BM && WC * 8 * kWaves == BN);
-  static_assert(BM % 64 == 0 && kWaves % (BM / 64) == 0 && S >= 2 && S <= 4 && (S - 2) * kOps < 64);
-  __shared__ __attribute__((aligned(1024))) uint8_t xl0[BM * kMmBlock], xl1[BM * kMmBlock], xl2[(S > 2 ? BM : 1) * kMmBlock],
-      xl3[(S > 3 ? BM : 1) * kMmBlock];
-  __shared__ __attribute__((aligned(1024))) uint8_t wl0[BN * kMmBlock], wl1[BN * kMmBlock], wl2[(S > 2 ? BN : 1) * kMmBlock],
-      wl3[(S > 3 ? BN : 1) * kMmBlock];
-  __shared__ __attribute__((aligned(256))) float sl0[BM], sl1[BM], sl2[S > 2 ? BM : 1], sl3[S > 3 ? BM : 1];
+  static_assert(BM % 64 == 0 && kWaves % (BM / 64) == 0 && (S == 2 || S == 3) && (S - 2) * kOps < 64);
+  __shared__ __attribute__((aligned(1024))) uint8_t xl0[BM * kMmBlock], xl1[BM * kMmBlock], xl2[(S > 2 ? BM : 1) * kMmBlock];
+  __shared__ __attribute__((aligned(1024))) uint8_t wl0[BN * kMmBlock], wl1[BN * kMmBlock], wl2[(S > 2 ? BN : 1) * kMmBlock];
+  __shared__ __attribute__((aligned(256))) float sl0[BM], sl1[BM], sl2[S > 2 ? BM : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
@@ -549,15 +547,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     scales();   // older than the copies: there when the first block's are
     copy(xl0, wl0, sl0, 0);
     if constexpr (S > 2) copy(xl1, wl1, sl1, 1);
-    if constexpr (S > 3) copy(xl2, wl2, sl2, 2);
     int b = 0;
     constexpr int kSpan = 60;   // blocks whose columns' scales are held at a time: whole rounds of the buffers
     for (;;) {
       for (; b + S <= min(a.kb, sw_first + kSpan); b += S) {
         turn(kLater);
         if constexpr (S == 2) copy(xl1, wl1, sl1, b + 1);
-        else if constexpr (S == 3) copy(xl2, wl2, sl2, b + 2);
-        else copy(xl3, wl3, sl3, b + 3);
+        else copy(xl2, wl2, sl2, b + 2);
         multiply(xl0, wl0, sl0, b);
         turn(kLater);
         copy(xl0, wl0, sl0, b + S);
@@ -566,11 +562,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
           turn(kLater);
           copy(xl1, wl1, sl1, b + S + 1);
           multiply(xl2, wl2, sl2, b + 2);
-        }
-        if constexpr (S > 3) {
-          turn(kLater);
-          copy(xl2, wl2, sl2, b + S + 2);
-          multiply(xl3, wl3, sl3, b + 3);
         }
       }
       if (sw_first + kSpan >= a.kb) break;
@@ -582,8 +573,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     if (b < a.kb) multiply(xl0, wl0, sl0, b);
     if constexpr (S > 2)
       if (b + 1 < a.kb) multiply(xl1, wl1, sl1, b + 1);
-    if constexpr (S > 3)
-      if (b + 2 < a.kb) multiply(xl2, wl2, sl2, b + 2);
 #pragma unroll
     for (int u = 0; u < kLag; ++u) add(kTiles - kLag + u, (kTiles - kLag + u) % kRing, s_prev);
 
@@ -599,7 +588,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 }
 
 // Tiles of 16 rows: the kernel of decode, where a matrix is read for a handful
-// of rows and its bytes are all that counts.  16 NT columns a workgroup; its WK
+// of rows and its bytes are all that counts.  16 columns a workgroup; its WK
 // wavefronts take turns along K, 4 blocks (512 bytes of each row of w) at a
 // time, all loads of the next turn requested before this one's products are
 // formed, straight into the registers that the products take them from.  The
@@ -609,11 +598,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // in a graph, 8.4 MB (1.9 TB/s): a launch (1.6 us) and two memory latencies,
 // and the joining; 64 x 64 tiles 6.8.  Not for experts: 32 rows of 128 experts
 // 100 us against the tile kernel's 60, whose copies need no registers.
-template <int NT, int WK, typename O>
+template <int WK, typename O>
 __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
-  constexpr int BN = 16 * NT, kTurn = 4;
-  static_assert(kMmBlock % BN == 0 && NT <= WK);
-  __shared__ f32x4 part[WK][NT][64];
+  constexpr int BN = 16, kTurn = 4;
+  __shared__ f32x4 part[WK][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
@@ -629,12 +617,10 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
   const float* sx = a.sx + (long long)(bad ? 0 : xr) * a.kb;
   const float* sw = a.sw + ((size_t)rt.expert * a.nb + n0 / kMmBlock) * a.kb;
   const rsrc_t wr = make_rsrc(a.w + (size_t)rt.expert * a.N * a.K, (uint64_t)a.N * a.K);
-  uint32_t wo[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) wo[i] = (uint32_t)min(n0 + 16 * i + lr, a.N - 1) * (uint32_t)a.K + 16u * lq;
+  const uint32_t wo = (uint32_t)min(n0 + lr, a.N - 1) * (uint32_t)a.K + 16u * lq;
 
   struct Turn {
-    u32x4 f[kTurn][NT][2], x[kTurn][2];
+    u32x4 f[kTurn][2], x[kTurn][2];
     float s[kTurn];
   };
   // blocks b .. b + 3; pieces behind K are zeros
@@ -645,9 +631,7 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool in = k + 64 * h + 16 * lq < a.K;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          t.f[c][i][h] = bload16<kStream>(wr, in ? wo[i] + (uint32_t)(k + 64 * h) : kMmOutOfRange, 0);
+        t.f[c][h] = bload16<kStream>(wr, in ? wo + (uint32_t)(k + 64 * h) : kMmOutOfRange, 0);
         t.x[c][h] = u32x4{{0, 0, 0, 0}};
         if (in) t.x[c][h] = *reinterpret_cast<const u32x4*>(x + k + 64 * h);
       }
@@ -655,9 +639,7 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
       t.s[c] = sx[bc] * sw[bc];
     }
   };
-  f32x4 acc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+  f32x4 acc{0, 0, 0, 0};
   auto join = [](const u32x4& u, const u32x4& v) {
     return i32x8_t{(int)u.v[0], (int)u.v[1], (int)u.v[2], (int)u.v[3], (int)v.v[0], (int)v.v[1], (int)v.v[2], (int)v.v[3]};
   };
@@ -665,12 +647,9 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
 #pragma unroll
     for (int c = 0; c < kTurn; ++c) {
       const float s = b + c < a.kb ? t.s[c] : 0.0f;
+      const f32x4 p = block_product<true>(join(t.f[c][0], t.f[c][1]), join(t.x[c][0], t.x[c][1]));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const f32x4 p = block_product<true>(join(t.f[c][i][0], t.f[c][i][1]), join(t.x[c][0], t.x[c][1]));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(p[j], s, acc[i][j]);
-      }
+      for (int j = 0; j < 4; ++j) acc[j] = __builtin_fmaf(p[j], s, acc[j]);
     }
   };
   Turn t0, t1;
@@ -684,16 +663,15 @@ __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
     if (b1 + kTurn * WK < a.kb) load(t0, b1 + kTurn * WK);
     multiply(t1, b1);
   }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) part[w][i][lane] = acc[i];
+  part[w][lane] = acc;
   __syncthreads();
-  if (w >= NT) return;
-  f32x4 v = part[0][w][lane];
+  if (w > 0) return;
+  f32x4 v = part[0][lane];
 #pragma unroll
-  for (int k = 1; k < WK; ++k) v += part[k][w][lane];
+  for (int k = 1; k < WK; ++k) v += part[k][lane];
   if (bad) v = f32x4{qnan(), qnan(), qnan(), qnan()};
   if (lr < rt.rows) {
-    const int n = n0 + 16 * w + 4 * lq;
+    const int n = n0 + 4 * lq;
     store4(static_cast<O*>(a.y) + (long long)(rt.first + lr) * a.ldy + n, v, a.N - n);
   }
 }
