@@ -40,7 +40,6 @@ constexpr int kBalSumThreads = 1024;
 constexpr int kBalSumWaves = kBalSumThreads / 64;
 constexpr int kBalSumCols = 32;       // experts that one workgroup of the second launch adds up, at least
 constexpr int kBalTargetParts = 512;  // workgroups of a pass: 2 per CU
-constexpr int kBalAhead = 1;          // rounds of rows that a wavefront has requested
 constexpr int kBalAlone = 256;        // tokens that one workgroup takes without a second launch
 
 constexpr int kBalMostTokens = 32768; // tokens of a part: what is added up in FP32
@@ -217,7 +216,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
     RowLoad<T, LR, V, C> r;
     uint32_t on;
     int id;   // this lane's slot of its row (l < k)
-  } rows[kBalAhead];
+  } rows;
   auto request = [&](Rows& q, int t) {
     const int c = min(t, S - 1);
     q.r.load(glogits + (long long)c * ld, E, l);
@@ -238,8 +237,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
     r -= r >= rounds ? rounds : 0;
     return (r * parts + part) * kStep + w * RW + rw;
   };
-#pragma unroll
-  for (int u = 0; u < kBalAhead; ++u) request(rows[u], token(min(u, rounds - 1)));
+  request(rows, token(0));
   for (int i = tid; i < kCols; i += kBalThreads) hist[i] = 0;
   if (!ALONE && blockIdx.x == 0 && tid == 0) *ticket = 0;
   __syncthreads();
@@ -256,23 +254,19 @@ __global__ __launch_bounds__(kBalThreads) void balance_parts_kernel(
   int nacc = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) P[v] = 0.0f;
-  for (int i = 0; i < rounds; i += kBalAhead) {
+  for (int i = 0; i < rounds; ++i) {
+    const int t = token(i);
+    const bool now = (t < S) & ((rows.on | all) != 0u);   // no branch: a load waited for in one is waited for at its end
+    float x[V], inv;
+    rows.r.values(x, E, l, now);
+    count(now & (l < k), rows.id);
+    request(rows, token(min(i + 1, rounds - 1)));   // behind the last round: that one again
+    __builtin_amdgcn_sched_barrier(0);              // before the work on this round, not after it
+    const float z = row_softmax<LR, V>(x, inv);
 #pragma unroll
-    for (int u = 0; u < kBalAhead; ++u) {
-      if (i + u >= rounds) break;
-      const int t = token(i + u);
-      const bool now = (t < S) & ((rows[u].on | all) != 0u);   // no branch: a load waited for in one is waited for at its end
-      float x[V], inv;
-      rows[u].r.values(x, E, l, now);
-      count(now & (l < k), rows[u].id);
-      request(rows[u], token(min(i + u + kBalAhead, rounds - 1)));   // behind the last round: that one again
-      __builtin_amdgcn_sched_barrier(0);         // before the work on this round, not after it
-      const float z = row_softmax<LR, V>(x, inv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) P[v] = __builtin_fmaf(x[v], inv, P[v]);
-      zacc = __builtin_fmaf(z, z, zacc);
-      nacc += now ? 1 : 0;
-    }
+    for (int v = 0; v < V; ++v) P[v] = __builtin_fmaf(x[v], inv, P[v]);
+    zacc = __builtin_fmaf(z, z, zacc);
+    nacc += now ? 1 : 0;
   }
   // the wavefront's row groups first (lanes l, l + LR, ...), then the wavefronts
   if constexpr (LR == 16) {
@@ -487,7 +481,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
   struct Rows {
     RowLoad<T, LR, V, C> r;
     uint32_t on;
-  } rows[kBalAhead];
+  } rows;
   const uint32_t all = valid ? 0u : 1u;   // every token counts
   const uint8_t* gvalid = valid ? valid + base : reinterpret_cast<const uint8_t*>(logits);   // any byte: not looked at
   auto request = [&](Rows& q, int t) {
@@ -506,8 +500,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
     r -= r >= rounds ? rounds : 0;
     return (r * parts + part) * kStep + w * RW + rw;
   };
-#pragma unroll
-  for (int u = 0; u < kBalAhead; ++u) request(rows[u], token(min(u, rounds - 1)));
+  request(rows, token(0));
   const float n = (float)max(tokens[g], 1), N = (float)max(tokens[G], 1);
   const float fb = grad_losses[0] * ((float)E / ((float)G * (float)k * n * n));
   const float zc = grad_losses[1] * (2.0f / N);
@@ -519,48 +512,44 @@ __global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) F[v] = balance_col<LR, C>(l, v) < E ? fb * F[v] : 0.0f;
-  for (int i = 0; i < rounds; i += kBalAhead) {
+  for (int i = 0; i < rounds; ++i) {
+    const int t = token(i);
+    const bool in = t < S, now = in & ((rows.on | all) != 0u);
+    float x[V], inv;
+    rows.r.values(x, E, l, now);
+    request(rows, token(min(i + 1, rounds - 1)));   // behind the last round: that one again
+    __builtin_amdgcn_sched_barrier(0);              // before the work on this round, not after it
+    const float z = row_softmax<LR, V>(x, inv);
+    float dot = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kBalAhead; ++u) {
-      if (i + u >= rounds) break;
-      const int t = token(i + u);
-      const bool in = t < S, now = in & ((rows[u].on | all) != 0u);
-      float x[V], inv;
-      rows[u].r.values(x, E, l, now);
-      request(rows[u], token(min(i + u + kBalAhead, rounds - 1)));   // behind the last round: that one again
-      __builtin_amdgcn_sched_barrier(0);         // before the work on this round, not after it
-      const float z = row_softmax<LR, V>(x, inv);
-      float dot = 0.0f;
+    for (int v = 0; v < V; ++v) dot = __builtin_fmaf(x[v], F[v], dot);
+    dot = row_sum<LR>(dot) * inv;
+    const float zt = zc * z - dot;
 #pragma unroll
-      for (int v = 0; v < V; ++v) dot = __builtin_fmaf(x[v], F[v], dot);
-      dot = row_sum<LR>(dot) * inv;
-      const float zt = zc * z - dot;
+    for (int v = 0; v < V; ++v) x[v] = now ? x[v] * inv * (F[v] + zt) : 0.0f;
+    if (!in) continue;
+    T* out = dlogits + (base + t) * ld_d;
+    if constexpr (C == 4) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = now ? x[v] * inv * (F[v] + zt) : 0.0f;
-      if (!in) continue;
-      T* out = dlogits + (base + t) * ld_d;
-      if constexpr (C == 4) {
-#pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-          const int c = balance_col<LR, 4>(l, 4 * q);
-          if (c >= E) continue;
-          if constexpr (sizeof(T) == 4) {
-            __builtin_nontemporal_store(f32_quad{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]},
-                                        reinterpret_cast<f32_quad*>(out + c));
-          } else {
-            __builtin_nontemporal_store(u32_pair{f32_to_bf16_rne(x[4 * q]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 1]) << 16,
-                                                 f32_to_bf16_rne(x[4 * q + 2]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 3]) << 16},
-                                        reinterpret_cast<u32_pair*>(out + c));
-          }
+      for (int q = 0; q < V / 4; ++q) {
+        const int c = balance_col<LR, 4>(l, 4 * q);
+        if (c >= E) continue;
+        if constexpr (sizeof(T) == 4) {
+          __builtin_nontemporal_store(f32_quad{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]},
+                                      reinterpret_cast<f32_quad*>(out + c));
+        } else {
+          __builtin_nontemporal_store(u32_pair{f32_to_bf16_rne(x[4 * q]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 1]) << 16,
+                                               f32_to_bf16_rne(x[4 * q + 2]) | (uint32_t)f32_to_bf16_rne(x[4 * q + 3]) << 16},
+                                      reinterpret_cast<u32_pair*>(out + c));
         }
-      } else {
+      }
+    } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = balance_col<LR, 1>(l, v);
-          if (c < E) {
-            if constexpr (sizeof(T) == 4) out[c] = x[v];
-            else out[c] = f32_to_bf16_rne(x[v]);
-          }
+      for (int v = 0; v < V; ++v) {
+        const int c = balance_col<LR, 1>(l, v);
+        if (c < E) {
+          if constexpr (sizeof(T) == 4) out[c] = x[v];
+          else out[c] = f32_to_bf16_rne(x[v]);
         }
       }
     }
