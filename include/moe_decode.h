@@ -355,8 +355,11 @@ int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q,
  *   w   uint8 [N, K] E4M3 codes
  *   sw  fp32 [ceil(N / 128), ceil(K / 128)]
  *   y   [M, N] of y_dtype (MOE_F32, MOE_BF16 or MOE_F16), row m at m * ldy elements
- * K a multiple of 16, x and w 16-byte aligned, ldx a multiple of 16.  The
- * gradient with respect to x is the same product with w and sw transposed.
+ * K a multiple of 16, x and w 16-byte aligned, ldx a multiple of 16.
+ * The gradient with respect to x is a product of the same kind: of dy, quantised
+ * in blocks of 128 along N (N a multiple of 16), with w^T [K, N] and sw^T [ceil(K /
+ * 128), ceil(N / 128)], which the caller lays out.  (With experts it is one row for
+ * each row of y; a row of x that several of them come from gets their sum.)
  *
  * moe_decode_matmul_fp8_experts: the same for E matrices w [E, N, K], sw [E,
  * ceil(N / 128), ceil(K / 128)] on rows sorted by expert: the first counts[0]
