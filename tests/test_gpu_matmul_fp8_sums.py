@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import moe_gate_up_amd as mg
-from tests.test_gpu_matmul_fp8 import F8, TYPES, values
+from tests.test_gpu_matmul_fp8 import F8, TYPES, grouped, values
 
 pytestmark = pytest.mark.gpu
 FP32_SUMS = {"built in": None, "rows": mg.MOE_MATMUL_ROWS_16, "64x64": mg.MOE_MATMUL_TILE_64X64, "64x128": mg.MOE_MATMUL_TILE_64X128,
@@ -149,3 +149,12 @@ def test_a_variant_gives_a_row_the_same_bits_for_every_number_of_rows(dev):
             whole = run(M, v)
             for m in (1, 2, 17, 65, 129, 299):
                 assert torch.equal(run(m, v), whole[:m]), (v, m)
+
+
+@pytest.mark.parametrize("variant", [0] + sorted(set(FP32_SUMS.values()) - {None}) + [mg.MOE_MATMUL_FP8_SUMS, mg.MOE_MATMUL_TILE_256X256])
+@pytest.mark.parametrize("shape", [(32, 128, 8, 192, 512, 0.0, 0), (40, 100, 6, 130, 272, 1.0, 7), (333, 7, 3, 129, 400, 0.5, 0)], ids=str)
+def test_experts_fp16(dev, shape, variant):
+    tokens, E, k, N, K, skew, extra = shape
+    for gather in (True, False):
+        print(f"experts {shape} f16 gather {gather} variant {variant}", flush=True)
+        grouped(dev, tokens, E, k, N, K, "f16", variant, gather, skew, extra)
