@@ -38,3 +38,43 @@ def test_error_at_every_size_of_gate(dev):
     assert float(use.max()) <= 1
     want = torch.where(v < 0, 0xFE, 0x7E).to(torch.uint8)      # 448, or -448
     assert torch.equal(q[:, 0].cpu(), want)
+
+
+def power_of_two(s):
+    """The smallest power of two that is not below s (float64; frexp: s = m 2^e, 1/2 <= m < 1)."""
+    m, e = torch.frexp(s)
+    return torch.where(m == 0.5, s, torch.ldexp(torch.ones_like(s), e))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("shape", [(1, 128), (5, 136), (65, 768), (9, 100), (33, 257)], ids=str)
+def test_rows_apart_and_powers_of_two(dev, shape, dtype):
+    """Rows with columns between them, a start that 16-byte loads cannot take, and power-of-two scales: the same codes and
+    scales as of the packed rows, and those within their bounds.  A code's value is within half a step (2^-4 relative, or
+    2^-10 scales among E4M3's subnormals) of v and v's own error."""
+    M, K = shape
+    g = torch.Generator().manual_seed(M + K)
+    x = (3 * torch.randn(M, 2 * K, generator=g)).to(dtype)
+    v = torch.sigmoid(x[:, :K].double()) * x[:, :K].double() * x[:, K:].double()
+    err = v.abs() * (3.5 + x[:, :K].double().abs() / 43) * 2.0 ** -23 + 1e-36
+    for pow2 in (False, True):
+        first = None
+        for pad, off in ((0, 0), (8, 0), (3, 0), (8, 1)):
+            print(f"SwiGLU {shape} {dtype} pow2 {pow2} pads {pad} {off}", flush=True)
+            wide = torch.full((M, 2 * K + pad + off), float("nan"), dtype=dtype, device=dev)
+            wide[:, off:off + 2 * K] = x.to(dev)
+            q = torch.full((M, K), 0xAA, dtype=torch.uint8, device=dev)
+            s = torch.full((M, -(-K // 128)), -1.0, device=dev)
+            mg.moe_decode_quantize_fp8(wide[:, off:off + 2 * K], q, s, swiglu=True, pow2=pow2)
+            first = first or (q, s)
+            assert torch.equal(q, first[0]) and torch.equal(s, first[1])
+        q, s = first[0].cpu(), first[1].cpu().double()
+        blocks = lambda t: torch.nn.functional.pad(t, (0, -K % 128)).view(M, -1, 128).amax(-1)   # noqa: E731
+        low, high = blocks((v.abs() - err).clamp_min(0)) / 448 * (1 - 2.0 ** -24), blocks(v.abs() + err) / 448 * (1 + 2.0 ** -24)
+        if pow2:
+            low, high = power_of_two(low), power_of_two(high)
+        assert bool(((low <= s) & (s <= high)).all())
+        each = s.repeat_interleave(128, 1)[:, :K]
+        back = q.view(torch.float8_e4m3fn).double() * each
+        tol = torch.maximum(v.abs() * 2.0 ** -4, each * 2.0 ** -10) * (1 + 2.0 ** -20) + err * (1 + 2.0 ** -4)
+        assert bool(((back - v).abs() <= tol).all())
