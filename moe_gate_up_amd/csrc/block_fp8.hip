@@ -137,7 +137,7 @@ bool tile_allowed(const moe::MatmulArgs& a, int bm) {
 // stated; the variants that the rule chooses between, its choice first).
 // One matrix: the smallest tiles while larger ones would leave CUs without
 // work, then the largest that still fill the chip.
-//   16 rows: M = 1, N = 4096 4.4, 64 x 64 6.8; M = 32, N = 4096 (512
+//   16 rows: M = 1, N = 4096 4.5, 64 x 64 9.4; M = 32, N = 4096 (512
 //     workgroups) 7.8, 9.8; M = 64, N = 2048, K = 4096 (512) 14.0, 17.1; but M =
 //     48, N = 4096 (768) 10.7, 10.2
 //   64 x 64: N = 4096, M = 256 (256 workgroups) 10.9, 64 x 128 14.4; M = 768

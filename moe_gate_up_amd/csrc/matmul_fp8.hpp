@@ -71,11 +71,11 @@ __device__ __forceinline__ MmTile tile_of_matrix(const MatmulArgs& a, int n_tile
 // tile of rows after the other.  How many tiles that makes is known on the
 // device only, and the grid is what it can be at most; the XCDs share out the
 // tiles that there are (by the grid, the last of them would have none: 128
-// experts of 1536 x 2048 and 32768 rows, 238 against 204 us).  Large tiles with
-// few rows in them come last, so that what a CU is left with at the end is
-// short (the same case 179 -> 177 us, 16384 rows 142 -> 135).  A wavefront looks at 64 experts at a time (the counts of 256
-// requested at once): prefix sums over the lanes give each expert's first tile
-// of both kinds and first row.
+// experts of 1536 x 2048 and 32768 rows, FP8 sums, 238 against 204 us).  Large
+// tiles with few rows in them come last, so that what a CU is left with at the end
+// is short (the same case 179 -> 177 us, 16384 rows 142 -> 135).  A wavefront looks
+// at 64 experts at a time (the counts of 256 requested at once): prefix sums over
+// the lanes give each expert's first tile of both kinds and first row.
 template <int BM>
 __device__ __forceinline__ MmTile tile_of_experts(const MatmulArgs& a, int n_tiles, int lane) {
   constexpr int kShort = BM >= 128 ? BM / 4 : 0;   // most rows of a tile that comes last
@@ -308,8 +308,9 @@ __device__ __forceinline__ void copy4_to_lds(rsrc_t r, void* lds, uint32_t voff,
 // A row number outside x makes its row NaN.  As they are, a lane's 4 results of
 // a 16-bit type are 8 bytes, and a store 16 rows of 32 bytes; by way of LDS, 16
 // rows at a time, in a space of the wavefront's own, it is whole rows of the
-// wavefront's columns, 16 bytes a lane, at any alignment (5734 x 3855, K = 1696:
-// 97 -> 66 us against stores of 2 bytes; FP32, 777 x 1003, K = 1040 9.3 -> 7.9).
+// wavefront's columns, 16 bytes a lane, at any alignment (5734 x 3855, K = 1696,
+// FP8 sums: 97 -> 66 us against stores of 2 bytes; an FP32 result, 777 x 1003, K =
+// 1040 9.3 -> 7.9).
 // STREAM: past the caches, which keep the operands for the tiles to come (with
 // FP8 sums 8192 rows, N = K = 4096: 138 -> 128 us; 4096 tokens through 128
 // experts, both products with the quantisation that reads the first's result
@@ -382,10 +383,10 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const MmTile& rt
 // are one number a block and wavefront (its columns lie in one block of 128):
 // lane l holds that of block l of the current span.
 //
-// FP32 sums, 128 x 128 (two workgroups a CU), 8192 rows, N = K = 4096: 229 us,
-// 1200 TFLOP/s (a library's bf16 product reaches 1471); a block has 64 matrix
-// instructions of a wavefront beside 128 conversions of codes, made by each of the
-// two wavefronts that share a row or a column.
+// FP32 sums, 128 x 128 (two workgroups a CU), 8192 rows, N = K = 4096: 229 to 243
+// us by box, 1130 to 1200 TFLOP/s (a library's bf16 product reaches 1471); a block
+// has 64 matrix instructions of a wavefront beside 128 conversions of codes, made
+// by each of the two wavefronts that share a row or a column.
 // Sums of the FP8 instruction, 256 x 256, the same case: 124 to 136 us (the matrix
 // cores alone, on the same codes and with the same scaling, 3700 TFLOP/s; with the
 // scaling left out 3950).  A workgroup takes 3580 cycles for a block whose products
@@ -594,10 +595,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // formed, straight into the registers that the products take them from.  The
 // wavefronts' sums are added in LDS, in their order.  w is read once, as
 // streaming data; the sums are always FP32 ones: the matrix cores wait for memory
-// all the same.  M = 1, N = 4096, K = 2048: 4.4 us
-// in a graph, 8.4 MB (1.9 TB/s): a launch (1.6 us) and two memory latencies,
-// and the joining; 64 x 64 tiles 6.8.  Not for experts: 32 rows of 128 experts
-// 100 us against the tile kernel's 60, whose copies need no registers.
+// all the same.  M = 1, N = 4096, K = 2048: 4.5 us in a graph, 8.4 MB (1.9 TB/s): a
+// launch (1.6 us) and two memory latencies, and the joining.  Not for experts: 2
+// rows of each of 128 experts of 1536 x 2048 100 us against the tile kernel's 56,
+// whose copies need no registers.
 template <int WK, typename O>
 __global__ __launch_bounds__(64 * WK) void matmul_rows_kernel(MatmulArgs a) {
   constexpr int BN = 16, kTurn = 4;
