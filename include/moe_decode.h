@@ -369,20 +369,18 @@ int moe_decode_quantize_fp8(const void *x, long long ldx, int dtype, uint8_t *q,
  * groups' added up, they go with those slots sorted by expert and the slots of
  * tokens that are not valid, or of other ids, behind them all, where they are not
  * computed.  (Slots of padding sorted in among the others would shift every later
- * expert's rows.)  Row m
- * of y comes from row m of x, or from row x_rows[m] where x_rows (int32 [M])
- * is given; x and sx have X rows.  A row number outside [0, X) is not read
- * through: its row of y is NaN.  Rows of y behind the last expert's are left
- * as they were; negative counts are taken as 0, and rows beyond M are not
+ * expert's rows.)  Row m of y comes from row m of x, or from row x_rows[m] where
+ * x_rows (int32 [M]) is given; x and sx have X rows.  A row number outside [0, X)
+ * is not read through: its row of y is NaN.  Rows of y behind the last expert's are
+ * left as they were; negative counts are taken as 0, and rows beyond M are not
  * computed.
  * Limits: E <= 1024, N * K < 2^31, M < 2^24 (experts) or 2^30, K <= 2^30, strides
  * up to 2^30, and of the tiles that y is cut into fewer than 2^24 (2^22 of
- * ROWS_16 and TILE_256X256).
- * M == 0 is a valid no-op.
+ * ROWS_16 and TILE_256X256).  M == 0 is a valid no-op.
  *
- * Kernel variants (the _ex forms take one; 0 = the built-in choice, the
- * fastest measured; moe_decode_matmul_fp8_plan reports it for ordinary
- * strides, E = 0 asking about one matrix):
+ * Kernel variants (the _ex forms take one; 0 = the built-in choice, by the
+ * sizes; moe_decode_matmul_fp8_plan reports it for ordinary strides, E = 0
+ * asking about one matrix):
  *   MOE_MATMUL_ROWS_16: 16 rows a workgroup, its wavefronts sharing out K.
  *   MOE_MATMUL_TILE_<rows>X<columns>: a tile of y a workgroup, both operands
  *     through LDS; _STREAM reads w as data that is used once.
