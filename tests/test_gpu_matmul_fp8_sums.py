@@ -158,3 +158,26 @@ def test_experts_fp16(dev, shape, variant):
     for gather in (True, False):
         print(f"experts {shape} f16 gather {gather} variant {variant}", flush=True)
         grouped(dev, tokens, E, k, N, K, "f16", variant, gather, skew, extra)
+
+
+def test_more_than_2_to_22_tiles(dev):
+    """One column for 2^29 + 129 rows, in 2^22 + 2 tiles of 128: codes of whole numbers, so that every sum is exact."""
+    M, K = (1 << 29) + 129, 16
+    print(f"M={M} N=1 K={K}", flush=True)
+    g = torch.Generator(device=dev).manual_seed(2)
+    table = torch.tensor([-2.0, -1.0, 0.0, 1.0, 2.0], device=dev).to(F8).view(torch.uint8)
+    few = torch.randint(0, 5, (1 << 20, K), generator=g, device=dev)
+    x = table[few].repeat(M // few.shape[0] + 1, 1)[:M]
+    x[-1] = table[4]
+    w = table[torch.randint(0, 5, (1, K), generator=g, device=dev)]
+    sx = torch.ones(M, 1, device=dev)
+    sx[1 << 29:] = 4
+    y = torch.full((M, 1), 7.0, dtype=torch.bfloat16, device=dev)
+    assert mg.moe_decode_matmul_fp8_plan(M, 1, K) == (mg.MOE_MATMUL_TILE_128X128, (1 << 22) + 2)
+    mg.moe_decode_matmul_fp8(x, sx, w, torch.ones(1, 1, device=dev), y)
+    torch.cuda.synchronize()
+    wv = w.view(F8).float()
+    for a in range(0, M, 1 << 26):
+        part = slice(a, min(a + (1 << 26), M))
+        ref = (x[part].view(F8).float() * wv).sum(1, keepdim=True) * sx[part]
+        assert torch.equal(y[part], ref.to(torch.bfloat16)), a
