@@ -49,7 +49,8 @@
  *     of the no-allocation entry point's scratch array (whose concurrent
  *     calls on one device race; see moe_decode_conventional_noalloc).
  *   - Outputs are fully overwritten; every element is written exactly once.
- *   - Outputs must not overlap any input (checked on the host).
+ *   - Outputs must not overlap any input (checked on the host), but where a
+ *     call says that an output may be one of its inputs itself.
  *   - B == 0 is a valid no-op.
  *   - topk_ids outside [0, E) are not read through: every output that depends
  *     on such a slot is written as a quiet NaN.  Duplicate ids in one token
@@ -422,6 +423,141 @@ int moe_decode_matmul_fp8_experts_ex(const uint8_t *x, long long ldx, const floa
                                      void *y, long long ldy, int y_dtype, int X, int M, int N, int K, int E,
                                      int variant, void *stream);
 int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int *variant, int *workgroups);
+
+/* Routing to experts by scores.  From logits [T, E], with s_te = softmax(l_t)_e, or
+ * 1 / (1 + e^-l_te) with MOE_ROUTE_SIGMOID, and c_te = s_te + bias_e:
+ *   - the experts lie in `groups` groups of E / groups neighbours.  A group's score
+ *     is its largest c, or with MOE_ROUTE_GROUP_TOP2 the sum of its two largest (the
+ *     one, where one expert alone is not ruled out).  The top_groups groups with the
+ *     largest scores stay, the lower group first among equals.
+ *   - of their experts token t takes the k with the largest c, largest first, the
+ *     lower id first among equals: topk_ids[t, j].
+ *   - topk_weights[t, j] = scale * s of that expert (without the bias), with
+ *     MOE_ROUTE_RENORM over the sum of the k (0 where that sum is 0).
+ * Choices are those of c in 64 bits; without a bias, experts (and groups by their
+ * largest) go by the logits.  Weights are FP32.  A logit of -inf rules an expert
+ * out: it comes behind all others of the groups that stay, its score is 0, a group
+ * of such comes last.  Ids are always different from each other and in [0, E);
+ * with a logit of +inf or NaN in the row they and the weights are not specified
+ * otherwise.
+ *   logits        [T, E] of `dtype` (MOE_F32 or MOE_BF16), row t at t * ld elements
+ *   bias          fp32 [E] or NULL (0)
+ *   topk_ids      int32 [T, k];  topk_weights  fp32 [T, k]
+ * moe_decode_route_experts_backward: dlogits_te = sum_j grad_weights[t, j] *
+ * d topk_weights[t, j] / d l_te, with the choices as constants (the bias has no
+ * gradient).  topk_ids outside [0, E) contribute nothing; an expert that stands
+ * there twice gets both terms.  Of the flags SIGMOID and RENORM matter.
+ * Limits: E <= 1024, k <= 64, groups <= 64 and a divisor of E, k <= top_groups * E /
+ * groups, T < 2^26, T * k < 2^31, strides up to 2^30.  T == 0 is a valid no-op. */
+#define MOE_ROUTE_SIGMOID 1
+#define MOE_ROUTE_RENORM 2
+#define MOE_ROUTE_GROUP_TOP2 4
+int moe_decode_route_experts(const void *logits, long long ld, int dtype, const float *bias,
+                             int32_t *topk_ids, float *topk_weights, int T, int E, int k,
+                             int groups, int top_groups, int flags, float scale, void *stream);
+int moe_decode_route_experts_backward(const void *logits, long long ld, int dtype, const int32_t *topk_ids,
+                                      const float *grad_weights, void *dlogits, long long ld_d,
+                                      int T, int E, int k, int flags, float scale, void *stream);
+
+/* The slots of topk_ids [T, k] sorted by expert, and by their number t * k + j within
+ * an expert: the rows of moe_decode_matmul_fp8_experts, and where the results of a
+ * token's slots lie.
+ *   counts     int32 [E]     slots of each expert
+ *   x_rows     int32 [T * k] the token of each sorted row; -1 behind the last expert's
+ *   positions  int32 [T, k]  the sorted row of each slot; -1 where it is not counted
+ * Slots of a token with valid[t] == 0 (valid: uint8 [T] or NULL) and ids outside [0,
+ * E) are not counted.  Limits: E <= 1024, k <= 64, T * k < 2^24.  `workspace` is
+ * device memory of at least moe_decode_sort_slots_workspace() bytes, 256-byte
+ * aligned, used until the launches complete (calls that may overlap in time need one
+ * each); it need not be cleared, and where that says 0 bytes it is not looked at.
+ * T == 0 is a valid no-op that writes nothing. */
+int moe_decode_sort_slots_workspace(int T, int E, int k, size_t *bytes);
+int moe_decode_sort_slots(const int32_t *topk_ids, const uint8_t *valid, int32_t *counts, int32_t *x_rows,
+                          int32_t *positions, void *workspace, size_t workspace_bytes,
+                          int T, int E, int k, void *stream);
+
+/* The experts' rows back to their tokens:
+ *   y[t, n] = add[t, n] + sum_j weights[t, j] * rows[positions[t, j], n]
+ * in FP32, rounded once.  A position outside [0, M) contributes nothing (its weight
+ * is not looked at).
+ *   rows       [M, N] of `dtype` (MOE_F32, MOE_BF16 or MOE_F16), row m at m * ld_rows
+ *   positions  int32 [T, k];  weights  fp32 [T, k] or NULL (1: a sum of rows, as for
+ *              the gradient of a token that stands in several sorted rows)
+ *   add        [T, N] of `dtype` or NULL (0); it may be y itself, with y's stride
+ *   y          [T, N] of `dtype`
+ * moe_decode_combine_backward: drows[positions[t, j], n] = weights[t, j] * dy[t, n]
+ * and dweights[t, j] = sum_n dy[t, n] * rows[positions[t, j], n] (0 for a position
+ * outside [0, M)); the gradient of `add` is dy.  Rows that no slot names are left as
+ * they were; no two slots may name the same row (one of their values would be left).
+ * dweights NULL: not wanted, rows are not read.
+ * Limits: k <= 64, T * k < 2^24, M <= 2^24, T * ceil(N / 2048) < 2^24, N <= 2^28,
+ * strides up to 2^30.  T == 0 is a valid no-op. */
+int moe_decode_combine(const void *rows, long long ld_rows, int dtype, const int32_t *positions,
+                       const float *weights, const void *add, long long ld_add, void *y, long long ld_y,
+                       int M, int T, int N, int k, void *stream);
+int moe_decode_combine_backward(const void *dy, long long ld_dy, const void *rows, long long ld_rows, int dtype,
+                                const int32_t *positions, const float *weights, void *drows, long long ld_d,
+                                float *dweights, int M, int T, int N, int k, void *stream);
+
+/* Root-mean-square norm of rows, with the residual's addition in front and 8 bits
+ * behind:
+ *   r = x + residual, rounded to `dtype` (x itself without a residual)
+ *   rstd = 1 / sqrt(mean_c r_c^2 + eps)
+ *   v_c = r_c * rstd * weight_c      in FP32
+ *   sum = r,  y = v rounded to `dtype`,  q and scales = v as moe_decode_quantize_fp8
+ *   makes them of FP32 values (MOE_QUANT_POW2 among its flags)
+ * Squares whose sum passes FP32 are added in FP64.  A NaN or an infinity in a row goes
+ * where the formula takes it.
+ *   x, residual, y, sum  [M, H] of `dtype` (MOE_F32, MOE_BF16 or MOE_F16), each with
+ *              its stride; residual, y and sum may be NULL (sum goes with a residual;
+ *              y or q is asked for); sum may be the residual itself, with its stride
+ *   weight     [H] of weight_dtype: `dtype` or MOE_F32
+ *   q          uint8 [M, H] E4M3 codes, scales fp32 [M, ceil(H / 128)], or both NULL
+ *   rstd       fp32 [M] or NULL
+ *   eps        a positive normal number up to 2^126
+ * moe_decode_rms_norm_backward, from dy [M, H], r as it was stored (sum, or x) and
+ * rstd, n_c = r_c * rstd:
+ *   dx_c = rstd * (dy_c weight_c - n_c * mean_i dy_i weight_i n_i) + dsum_c
+ *   dweight_c = sum_m dy_mc n_mc     fp32 [H], the rows' sums in a fixed order
+ * dx is the gradient of x and of the residual.  dsum (the gradient that reaches `sum`
+ * from elsewhere) may be NULL (0), or dx itself with its stride.  `workspace` is device memory
+ * of at least moe_decode_rms_norm_backward_workspace() bytes, 256-byte aligned, used
+ * until the launches complete (calls that may overlap in time need one each); it need
+ * not be cleared.
+ * Limits: H <= 32768; M < 2^26 up to 4096 columns, 2^24 up to 16384, else 2^22;
+ * strides up to 2^30.  M == 0 is a valid no-op that writes nothing. */
+int moe_decode_rms_norm(const void *x, long long ld_x, const void *residual, long long ld_residual, int dtype,
+                        const void *weight, int weight_dtype, float eps, void *y, long long ld_y,
+                        uint8_t *q, float *scales, void *sum, long long ld_sum, float *rstd,
+                        int M, int H, int flags, void *stream);
+int moe_decode_rms_norm_backward_workspace(int M, int H, size_t *bytes);
+int moe_decode_rms_norm_backward(const void *dy, long long ld_dy, const void *r, long long ld_r, int dtype,
+                                 const void *weight, int weight_dtype, const float *rstd,
+                                 const void *dsum, long long ld_dsum, void *dx, long long ld_dx, float *dweight,
+                                 void *workspace, size_t workspace_bytes, int M, int H, void *stream);
+
+/* Low-rank adapters of many requests beside a projection:
+ *   y[m, n] = base[m, n] + scaling[l] * sum_r b[l, n, r] * sum_c a[l, r, c] * x[m, c]
+ * with l = row_adapters[m]; a row whose l lies outside [0, L) gets the base alone.
+ * Both sums are FP32, the inner ones not rounded to 16 bits between the two (they
+ * enter the second as the sum of two 16-bit numbers, to 2^-16 of themselves, in FP16
+ * of the row's largest), and the result is rounded once.
+ *   x             [M, K] of `dtype` (MOE_BF16 or MOE_F16), row m at m * ld_x elements
+ *   row_adapters  int32 [M]
+ *   a             [L, R, K];  b  [L, N, R];  scaling  fp32 [L]
+ *   base          [M, N] of `dtype`, or NULL (0); it may be y itself, with y's stride
+ *   y             [M, N] of `dtype`
+ * K, R and ld_x multiples of 8; x, a and b 16-byte aligned.
+ * Limits: R <= 256, L <= 1023, M < 2^22, K and N <= 2^20, strides up to 2^30.
+ * `workspace` is device memory of at least moe_decode_adapters_workspace() bytes,
+ * 256-byte aligned, used until the launches complete (calls that may overlap in time
+ * need one each); it need not be cleared, and where that says 0 bytes it is not
+ * looked at.  M == 0 is a valid no-op. */
+int moe_decode_adapters_workspace(int M, int K, int N, int R, int L, size_t *bytes);
+int moe_decode_adapters(const void *x, long long ld_x, int dtype, const int32_t *row_adapters,
+                        const void *a, const void *b, const float *scaling,
+                        const void *base, long long ld_base, void *y, long long ld_y,
+                        void *workspace, size_t workspace_bytes, int M, int K, int N, int R, int L, void *stream);
 
 /* Bandwidth probes that set the denominator of the efficiency figure (blog
  * post, "Hardware efficiency": peak measured with a copy kernel over

@@ -46,6 +46,9 @@ MOE_MATMUL_TILE_128X128 = 5
 MOE_MATMUL_TILE_256X256 = 6
 MOE_MATMUL_FAR_ROWS = 7
 MOE_MATMUL_FP8_SUMS = 256
+MOE_ROUTE_SIGMOID = 1
+MOE_ROUTE_RENORM = 2
+MOE_ROUTE_GROUP_TOP2 = 4
 
 EXPORTS = (
     "moe_decode_gate_up", "moe_decode_down", "moe_decode_gate_up_ex", "moe_decode_down_ex",
@@ -54,6 +57,10 @@ EXPORTS = (
     "moe_decode_balance_workspace", "moe_decode_balance", "moe_decode_balance_backward", "moe_decode_quantize_fp8",
     "moe_decode_matmul_fp8", "moe_decode_matmul_fp8_ex", "moe_decode_matmul_fp8_experts",
     "moe_decode_matmul_fp8_experts_ex", "moe_decode_matmul_fp8_plan",
+    "moe_decode_route_experts", "moe_decode_route_experts_backward", "moe_decode_sort_slots_workspace",
+    "moe_decode_sort_slots", "moe_decode_combine", "moe_decode_combine_backward", "moe_decode_rms_norm",
+    "moe_decode_rms_norm_backward_workspace", "moe_decode_rms_norm_backward", "moe_decode_adapters_workspace",
+    "moe_decode_adapters",
     "moe_decode_copy_peak", "moe_decode_read_peak",
     "moe_decode_strerror",
 )
@@ -100,6 +107,18 @@ def lib() -> ctypes.CDLL:
             L.moe_decode_matmul_fp8_experts.argtypes = [P, LL] + [P] * 6 + [LL] + [I] * 6 + [P]
             L.moe_decode_matmul_fp8_experts_ex.argtypes = [P, LL] + [P] * 6 + [LL] + [I] * 7 + [P]
             L.moe_decode_matmul_fp8_plan.argtypes = [I] * 4 + [IP, IP]
+            SP, F = ctypes.POINTER(S), ctypes.c_float
+            L.moe_decode_route_experts.argtypes = [P, LL, I, P, P, P] + [I] * 6 + [F, P]
+            L.moe_decode_route_experts_backward.argtypes = [P, LL, I, P, P, P, LL] + [I] * 4 + [F, P]
+            L.moe_decode_sort_slots_workspace.argtypes = [I] * 3 + [SP]
+            L.moe_decode_sort_slots.argtypes = [P] * 6 + [S] + [I] * 3 + [P]
+            L.moe_decode_combine.argtypes = [P, LL, I, P, P, P, LL, P, LL] + [I] * 4 + [P]
+            L.moe_decode_combine_backward.argtypes = [P, LL, P, LL, I, P, P, P, LL, P] + [I] * 4 + [P]
+            L.moe_decode_rms_norm.argtypes = [P, LL, P, LL, I, P, I, F, P, LL, P, P, P, LL, P, I, I, I, P]
+            L.moe_decode_rms_norm_backward_workspace.argtypes = [I, I, SP]
+            L.moe_decode_rms_norm_backward.argtypes = [P, LL, P, LL, I, P, I, P, P, LL, P, LL, P, P, S, I, I, P]
+            L.moe_decode_adapters_workspace.argtypes = [I] * 5 + [SP]
+            L.moe_decode_adapters.argtypes = [P, LL, I, P, P, P, P, P, LL, P, LL, P, S] + [I] * 5 + [P]
             L.moe_decode_copy_peak.argtypes = [P, P, S, P]
             L.moe_decode_read_peak.argtypes = [P, S, P, P]
             L.moe_decode_strerror.argtypes = [I]
@@ -500,6 +519,213 @@ def moe_decode_matmul_fp8_plan(M, N, K, E=0):
     if rc:
         raise MoeDecodeError(rc, "moe_decode_matmul_fp8_plan")
     return v.value, g.value
+
+
+# ---------------------------------------------------------------- around the experts: router, slots, norm, adapters
+def moe_decode_route_experts(logits, topk_ids, topk_weights, bias=None, sigmoid=False, renorm=True, groups=1, top_groups=1,
+                             group_top2=False, scale=1.0, stream=None):
+    """topk_ids (int32) and topk_weights (fp32) [T,k] from the router's logits [T,E] (fp32 or bf16): the k largest of
+    softmax (or sigmoid) scores + bias [E] within the top_groups best groups of experts, weighted with the scores, over
+    their sum with renorm, times scale (see include/moe_decode.h)."""
+    L = _load()
+    d = _gpu(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    _call("moe_decode_route_experts", L.moe_decode_route_experts, d, stream, logits.data_ptr(),
+          _rows(logits, "logits", d, T, E), _dtype_code(logits, "logits", (MOE_F32, MOE_BF16)),
+          None if bias is None else _flat(bias, "bias", d, E, _f32), _flat(topk_ids, "topk_ids", d, T * k, _i32),
+          _flat(topk_weights, "topk_weights", d, (T, k), _f32), T, E, k, groups, top_groups,
+          (MOE_ROUTE_SIGMOID if sigmoid else 0) | (MOE_ROUTE_RENORM if renorm else 0) |
+          (MOE_ROUTE_GROUP_TOP2 if group_top2 else 0), scale)
+    return topk_ids, topk_weights
+
+
+def moe_decode_route_experts_backward(logits, topk_ids, grad_weights, dlogits, sigmoid=False, renorm=True, scale=1.0,
+                                      stream=None):
+    """dlogits [T,E] = the gradient of grad_weights [T,k] . topk_weights of moe_decode_route_experts with respect to the
+    logits, for the choices topk_ids it made (see include/moe_decode.h)."""
+    L = _load()
+    d = _gpu(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    dt = _dtype_code(logits, "logits", (MOE_F32, MOE_BF16))
+    if _codes.get(dlogits.dtype) != dt:
+        raise ValueError("dlogits must have the type of logits")
+    _call("moe_decode_route_experts_backward", L.moe_decode_route_experts_backward, d, stream, logits.data_ptr(),
+          _rows(logits, "logits", d, T, E), dt, _flat(topk_ids, "topk_ids", d, T * k, _i32),
+          _flat(grad_weights, "grad_weights", d, (T, k), _f32), dlogits.data_ptr(), _rows(dlogits, "dlogits", d, T, E),
+          T, E, k, (MOE_ROUTE_SIGMOID if sigmoid else 0) | (MOE_ROUTE_RENORM if renorm else 0), scale)
+    return dlogits
+
+
+@functools.lru_cache(maxsize=256)
+def moe_decode_sort_slots_workspace(T, E, k):
+    """Bytes of device workspace moe_decode_sort_slots needs."""
+    n = ctypes.c_size_t()
+    rc = lib().moe_decode_sort_slots_workspace(T, E, k, ctypes.byref(n))
+    if rc:
+        raise MoeDecodeError(rc, "moe_decode_sort_slots_workspace")
+    return n.value
+
+
+def _workspace(workspace, need, device, stream, where):
+    """(tensor or None, its bytes): the caller's workspace, or `need` bytes of torch's allocator on the current stream."""
+    if workspace is not None:
+        return _flat(workspace, "workspace", device, workspace.numel(), _u8), workspace.numel(), workspace
+    if not need:
+        return None, 0, None
+    if stream is not None:
+        raise ValueError(f"{where} on a given stream needs a workspace")
+    t = _torch.empty(need, dtype=_u8, device=device)
+    return t.data_ptr(), need, t
+
+
+def moe_decode_sort_slots(topk_ids, counts, x_rows, positions, valid=None, workspace=None, stream=None):
+    """The slots of topk_ids [T,k] sorted by expert, all int32: counts [E], x_rows [T*k] (the token of each sorted row, as
+    moe_decode_matmul_fp8_experts takes it) and positions [T,k] (the sorted row of each slot, as moe_decode_combine takes
+    it); -1 for slots of tokens that are not valid and for ids outside [0,E) (see include/moe_decode.h).
+
+    Without a workspace one is taken from torch's allocator for the call (which then runs on the current stream)."""
+    L = _load()
+    d = _gpu(topk_ids, "topk_ids")
+    T, k = topk_ids.shape
+    E = counts.shape[-1]
+    ws, n, keep = _workspace(workspace, moe_decode_sort_slots_workspace(T, E, k), d, stream, "moe_decode_sort_slots")
+    _call("moe_decode_sort_slots", L.moe_decode_sort_slots, d, stream, _flat(topk_ids, "topk_ids", d, (T, k), _i32),
+          None if valid is None else _flat(valid, "valid", d, T, _flags), _flat(counts, "counts", d, E, _i32),
+          _flat(x_rows, "x_rows", d, T * k, _i32), _flat(positions, "positions", d, (T, k), _i32), ws, n, T, E, k)
+    return counts, x_rows, positions
+
+
+def moe_decode_combine(rows, positions, weights, y, add=None, stream=None):
+    """y [T,N] = add + sum_j weights[:,j] * rows[positions[:,j]] of rows [M,N] (fp32, bf16 or fp16), positions int32 [T,k];
+    weights fp32 [T,k] or None (1); add may be y (see include/moe_decode.h)."""
+    L = _load()
+    d = _gpu(rows, "rows")
+    M, N = rows.shape
+    T, k = positions.shape
+    dt = _dtype_code(rows, "rows", (MOE_F32, MOE_BF16, MOE_F16))
+    if _codes.get(y.dtype) != dt or (add is not None and _codes.get(add.dtype) != dt):
+        raise ValueError("y and add must have the type of rows")
+    _call("moe_decode_combine", L.moe_decode_combine, d, stream, rows.data_ptr(), _rows(rows, "rows", d, M, N), dt,
+          _flat(positions, "positions", d, (T, k), _i32),
+          None if weights is None else _flat(weights, "weights", d, (T, k), _f32),
+          None if add is None else add.data_ptr(), 0 if add is None else _rows(add, "add", d, T, N),
+          y.data_ptr(), _rows(y, "y", d, T, N), M, T, N, k)
+    return y
+
+
+def moe_decode_combine_backward(dy, rows, positions, weights, drows, dweights, stream=None):
+    """drows [M,N] (rows that no slot names stay as they were) and dweights fp32 [T,k], the gradients of
+    moe_decode_combine from dy [T,N]; without dweights (None) rows may be None too (see include/moe_decode.h)."""
+    L = _load()
+    d = _gpu(dy, "dy")
+    T, N = dy.shape
+    M, k = drows.shape[0], positions.shape[-1]
+    dt = _dtype_code(dy, "dy", (MOE_F32, MOE_BF16, MOE_F16))
+    if dweights is not None and rows is None:
+        raise ValueError("dweights need rows")
+    if _codes.get(drows.dtype) != dt or (rows is not None and _codes.get(rows.dtype) != dt):
+        raise ValueError("rows and drows must have the type of dy")
+    _call("moe_decode_combine_backward", L.moe_decode_combine_backward, d, stream, dy.data_ptr(), _rows(dy, "dy", d, T, N),
+          None if rows is None else rows.data_ptr(), 0 if rows is None else _rows(rows, "rows", d, M, N), dt,
+          _flat(positions, "positions", d, (T, k), _i32),
+          None if weights is None else _flat(weights, "weights", d, (T, k), _f32),
+          drows.data_ptr(), _rows(drows, "drows", d, M, N),
+          None if dweights is None else _flat(dweights, "dweights", d, (T, k), _f32), M, T, N, k)
+    return drows, dweights
+
+
+def moe_decode_rms_norm(x, weight, eps, y=None, q=None, scales=None, residual=None, sum_out=None, rstd=None, pow2=False,
+                        stream=None):
+    """The root-mean-square norm of x [M,H] (+ residual) times weight [H] (x's type or fp32): y [M,H], and / or q [M,H]
+    E4M3 codes (uint8) with scales fp32 [M, ceil(H/128)]; sum_out [M,H]: x + residual (it may be the residual); rstd
+    fp32 [M] (see include/moe_decode.h)."""
+    L = _load()
+    d = _gpu(x, "x")
+    M, H = x.shape
+    dt = _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16))
+    p = [x.data_ptr(), _rows(x, "x", d, M, H)]
+    for t, name in ((residual, "residual"), (y, "y"), (sum_out, "sum_out")):
+        if t is None:
+            p += [None, 0]
+        else:
+            if _codes.get(t.dtype) != dt:
+                raise ValueError(f"{name} must have the type of x")
+            p += [t.data_ptr(), _rows(t, name, d, M, H)]
+    wt = _dtype_code(weight, "weight", (MOE_F32, dt))
+    _call("moe_decode_rms_norm", L.moe_decode_rms_norm, d, stream, *p[:4], dt, _flat(weight, "weight", d, H, weight.dtype),
+          wt, eps, *p[4:6], None if q is None else _flat(q, "q", d, (M, H), _u8),
+          None if scales is None else _flat(scales, "scales", d, (M, -(-H // 128)), _f32), *p[6:],
+          None if rstd is None else _flat(rstd, "rstd", d, M, _f32), M, H, MOE_QUANT_POW2 if pow2 else 0)
+
+
+@functools.lru_cache(maxsize=256)
+def moe_decode_rms_norm_backward_workspace(M, H):
+    """Bytes of device workspace moe_decode_rms_norm_backward needs."""
+    n = ctypes.c_size_t()
+    rc = lib().moe_decode_rms_norm_backward_workspace(M, H, ctypes.byref(n))
+    if rc:
+        raise MoeDecodeError(rc, "moe_decode_rms_norm_backward_workspace")
+    return n.value
+
+
+def moe_decode_rms_norm_backward(dy, r, weight, rstd, dx, dweight, dsum=None, workspace=None, stream=None):
+    """dx [M,H] (the gradient of x and of the residual) and dweight fp32 [H] of moe_decode_rms_norm from dy [M,H], r (its
+    sum_out, or x where it had no residual) and rstd; dsum [M,H]: the gradient that reaches sum_out from elsewhere, which
+    may be dx (see include/moe_decode.h).
+
+    Without a workspace one is taken from torch's allocator for the call (which then runs on the current stream)."""
+    L = _load()
+    d = _gpu(dy, "dy")
+    M, H = dy.shape
+    dt = _dtype_code(dy, "dy", (MOE_F32, MOE_BF16, MOE_F16))
+    for t, name in ((r, "r"), (dx, "dx"), (dsum, "dsum")):
+        if t is not None and _codes.get(t.dtype) != dt:
+            raise ValueError(f"{name} must have the type of dy")
+    ws, n, keep = _workspace(workspace, moe_decode_rms_norm_backward_workspace(M, H) if M else 0, d, stream,
+                             "moe_decode_rms_norm_backward")
+    _call("moe_decode_rms_norm_backward", L.moe_decode_rms_norm_backward, d, stream, dy.data_ptr(),
+          _rows(dy, "dy", d, M, H), r.data_ptr(), _rows(r, "r", d, M, H), dt,
+          _flat(weight, "weight", d, H, weight.dtype), _dtype_code(weight, "weight", (MOE_F32, dt)),
+          _flat(rstd, "rstd", d, M, _f32), None if dsum is None else dsum.data_ptr(),
+          0 if dsum is None else _rows(dsum, "dsum", d, M, H), dx.data_ptr(), _rows(dx, "dx", d, M, H),
+          _flat(dweight, "dweight", d, H, _f32), ws, n, M, H)
+    return dx, dweight
+
+
+@functools.lru_cache(maxsize=256)
+def moe_decode_adapters_workspace(M, K, N, R, L):
+    """Bytes of device workspace moe_decode_adapters needs."""
+    n = ctypes.c_size_t()
+    rc = lib().moe_decode_adapters_workspace(M, K, N, R, L, ctypes.byref(n))
+    if rc:
+        raise MoeDecodeError(rc, "moe_decode_adapters_workspace")
+    return n.value
+
+
+def moe_decode_adapters(x, row_adapters, a, b, scaling, y, base=None, workspace=None, stream=None):
+    """y [M,N] = base + scaling[l] * (x a[l]^T) b[l]^T for each row's adapter l = row_adapters[m] (int32; outside [0,L):
+    none), x [M,K], a [L,R,K], b [L,N,R] (bf16 or fp16), scaling fp32 [L]; base [M,N] or None (0), which may be y (see
+    include/moe_decode.h).
+
+    Without a workspace one is taken from torch's allocator for the call (which then runs on the current stream)."""
+    lb = _load()
+    d = _gpu(x, "x")
+    M, K = x.shape
+    L, R = a.shape[0], a.shape[1]
+    N = b.shape[1]
+    dt = _dtype_code(x, "x", (MOE_BF16, MOE_F16))
+    for t, name in ((a, "a"), (b, "b"), (y, "y"), (base, "base")):
+        if t is not None and _codes.get(t.dtype) != dt:
+            raise ValueError(f"{name} must have the type of x")
+    ws, n, keep = _workspace(workspace, moe_decode_adapters_workspace(M, K, N, R, L), d, stream, "moe_decode_adapters")
+    _call("moe_decode_adapters", lb.moe_decode_adapters, d, stream, x.data_ptr(), _rows(x, "x", d, M, K), dt,
+          _flat(row_adapters, "row_adapters", d, M, _i32), _flat(a, "a", d, (L, R, K), a.dtype),
+          _flat(b, "b", d, (L, N, R), b.dtype), _flat(scaling, "scaling", d, L, _f32),
+          None if base is None else base.data_ptr(), 0 if base is None else _rows(base, "base", d, M, N),
+          y.data_ptr(), _rows(y, "y", d, M, N), ws, n, M, K, N, R, L)
+    return y
 
 
 def moe_decode_copy_peak(src, dst, stream=None):

@@ -17,6 +17,10 @@ SOURCES = [
     ("moe_decode.hip", []),
     ("balance.hip", []),
     ("block_fp8.hip", []),
+    ("route_experts.hip", []),
+    ("rms_norm.hip", []),
+    ("rms_norm_backward.hip", []),
+    ("adapters.hip", []),
     ("down_token.hip", ["-mllvm", "-amdgpu-sched-strategy=max-memory-clause"]),
     ("down_mfma.hip", ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]),
 ]

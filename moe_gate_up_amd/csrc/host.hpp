@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #pragma GCC visibility push(hidden)
@@ -37,6 +38,30 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return na && nb && x < y + nb && y < x + na;
 }
+
+constexpr long long kMaxStride = 1LL << 30;
+
+// A stretch of device memory; nullptr: none.
+struct Range {
+  const void* p;
+  size_t n;
+};
+// An output overlaps an input or another output.
+inline bool any_overlap(std::initializer_list<Range> out, std::initializer_list<Range> in) {
+  for (const Range* o = out.begin(); o != out.end(); ++o) {
+    if (!o->p) continue;
+    for (const Range& i : in)
+      if (i.p && overlaps(o->p, o->n, i.p, i.n)) return true;
+    for (const Range* p = out.begin(); p != o; ++p)
+      if (p->p && overlaps(o->p, o->n, p->p, p->n)) return true;
+  }
+  return false;
+}
+// Bytes from the first to the last element of M rows of n elements, ld apart.
+inline size_t rows_bytes(int M, int n, long long ld, size_t size) {
+  return M ? ((M > 1 ? (size_t)(M - 1) * (size_t)ld : 0) + (size_t)n) * size : 0;
+}
+inline bool rows_stride_ok(int M, int n, long long ld) { return M <= 1 || (ld >= n && ld <= kMaxStride); }
 
 // Runs f() once per device, on the first call made with that device current,
 // and returns its result on every call.

@@ -90,26 +90,8 @@ __device__ __forceinline__ float silu_exact(float g) {
   return g == -__builtin_huge_valf() ? -0.0f : v;
 }
 
-// Unit u = block u % nb of row u / nb; `magic` is ceil(2^32 / nb).
-template <typename T, bool SWIGLU, int FORM>
-__global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __restrict__ x, long long ldx,
-                                                                 uint8_t* __restrict__ q, float* __restrict__ scales,
-                                                                 int units, int K, int nb, uint32_t magic, bool pow2) {
-  const int l = threadIdx.x & 15;
-  const int u = (int)blockIdx.x * (kQuantThreads / kQuantLanes) + (int)(threadIdx.x / kQuantLanes);
-  if (u >= units) return;
-  int m = nb == 1 ? u : (int)__umulhi((uint32_t)u, magic);   // the quotient, or one more
-  m -= m * nb > u ? 1 : 0;
-  const int c = (u - m * nb) * kQuantBlock + l * kQuantPer, left = K - c;
-  const T* row = x + (long long)m * ldx + c;
-  float v[8];
-  load8<T, FORM>(row, left, v);
-  if constexpr (SWIGLU) {
-    float up[8];
-    load8<T, FORM>(row + K, left, up);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = silu_exact(v[j]) * up[j];
-  }
+// The codes of a block whose 8 elements a lane of 16 are v (first four in lo), and its scale.
+__device__ __forceinline__ float block_codes(float (&v)[8], bool pow2, uint32_t& lo, uint32_t& hi) {
   auto magnitude = [](float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; };
   uint32_t a = 0;
 #pragma unroll
@@ -142,9 +124,9 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __rest
   float r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = __builtin_copysignf(divide_by(v[j], d, inv), v[j]);   // -0 stays -0
-  uint32_t lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+  lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
   lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], (int)lo, true);
-  uint32_t hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
+  hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
   hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], (int)hi, true);
   if (odd) {   // NaN and infinities are the one NaN code 0x7F
 #pragma unroll
@@ -154,6 +136,31 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __rest
       else hi = (nan >> j & 1) ? (hi & ~mask) | code : hi;
     }
   }
+  return s;
+}
+
+// Unit u = block u % nb of row u / nb; `magic` is ceil(2^32 / nb).
+template <typename T, bool SWIGLU, int FORM>
+__global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T* __restrict__ x, long long ldx,
+                                                                 uint8_t* __restrict__ q, float* __restrict__ scales,
+                                                                 int units, int K, int nb, uint32_t magic, bool pow2) {
+  const int l = threadIdx.x & 15;
+  const int u = (int)blockIdx.x * (kQuantThreads / kQuantLanes) + (int)(threadIdx.x / kQuantLanes);
+  if (u >= units) return;
+  int m = nb == 1 ? u : (int)__umulhi((uint32_t)u, magic);   // the quotient, or one more
+  m -= m * nb > u ? 1 : 0;
+  const int c = (u - m * nb) * kQuantBlock + l * kQuantPer, left = K - c;
+  const T* row = x + (long long)m * ldx + c;
+  float v[8];
+  load8<T, FORM>(row, left, v);
+  if constexpr (SWIGLU) {
+    float up[8];
+    load8<T, FORM>(row + K, left, up);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = silu_exact(v[j]) * up[j];
+  }
+  uint32_t lo, hi;
+  const float s = block_codes(v, pow2, lo, hi);
   uint8_t* out = q + (long long)m * K + c;
   if constexpr (FORM == kQuantElements) {
 #pragma unroll

@@ -1,0 +1,104 @@
+// C ABI of the root-mean-square norm's gradients (rms_norm_backward.hpp): argument checks,
+// launch shapes and launches.  The contract is stated in include/moe_decode.h.
+#include "host.hpp"
+#include "norm_shape.hpp"
+#include "rms_norm_backward.hpp"
+
+namespace {
+
+using moe_host::aligned;
+using moe_host::any_overlap;
+using moe_host::rows_bytes;
+using moe_host::rows_stride_ok;
+
+size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
+
+constexpr int kParts = 512;   // workgroups, each with a row of the workspace
+
+struct Parts {
+  int M;
+  int* parts;
+  template <int WR, int P>
+  void operator()() const {
+    const int n = (M + moe::norm_rows(WR) - 1) / moe::norm_rows(WR);
+    *parts = n < kParts ? n : kParts;
+  }
+};
+int parts_of(int M, int H) {
+  int n = 0;
+  moe_host::by_row(H, Parts{M, &n});
+  return n;
+}
+
+template <typename T, typename W>
+struct Backward {
+  hipStream_t st;
+  const void *dy, *r, *weight, *dsum;
+  void* dx;
+  const moe::NormBackwardArgs& a;
+  int parts;
+  template <int WR, int P>
+  void operator()() const {
+    hipLaunchKernelGGL((moe::rms_norm_backward_kernel<T, W, WR, P>), dim3((unsigned)parts),
+                       dim3((unsigned)moe::norm_threads(WR)), 0, st, static_cast<const T*>(dy), static_cast<const T*>(r),
+                       static_cast<const W*>(weight), static_cast<const T*>(dsum), static_cast<T*>(dx), a);
+  }
+};
+template <typename T>
+void launch(hipStream_t st, const void* dy, const void* r, const void* weight, bool f32_weight, const void* dsum, void* dx,
+            const moe::NormBackwardArgs& a, int parts) {
+  if (f32_weight) moe_host::by_row(a.H, Backward<T, float>{st, dy, r, weight, dsum, dx, a, parts});
+  else moe_host::by_row(a.H, Backward<T, T>{st, dy, r, weight, dsum, dx, a, parts});
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_decode_rms_norm_backward_workspace(int M, int H, size_t* bytes) {
+  const int rc = moe_host::check_norm(M, H);
+  if (rc) return rc;
+  if (!bytes) return MOE_ERR_NULL;
+  *bytes = (size_t)parts_of(M, H) * H * 4;
+  return MOE_OK;
+}
+
+int moe_decode_rms_norm_backward(const void* dy, long long ld_dy, const void* r, long long ld_r, int dtype,
+                                 const void* weight, int weight_dtype, const float* rstd, const void* dsum,
+                                 long long ld_dsum, void* dx, long long ld_dx, float* dweight, void* workspace,
+                                 size_t workspace_bytes, int M, int H, void* stream) {
+  const int rc = moe_host::check_norm(M, H);
+  if (rc) return rc;
+  if (!dtype_ok(dtype) || (weight_dtype != MOE_F32 && weight_dtype != dtype)) return MOE_ERR_ARG;
+  if (M == 0) return MOE_OK;
+  if (!rows_stride_ok(M, H, ld_dy) || !rows_stride_ok(M, H, ld_r) || (dsum && !rows_stride_ok(M, H, ld_dsum)) ||
+      !rows_stride_ok(M, H, ld_dx))
+    return MOE_ERR_SHAPE;
+  if (!dy || !r || !weight || !rstd || !dx || !dweight || !workspace) return MOE_ERR_NULL;
+  const size_t size = dtype_size(dtype);
+  if (!aligned(dy, size) || !aligned(r, size) || !aligned(weight, dtype_size(weight_dtype)) || !aligned(rstd, 4) ||
+      !aligned(dsum, size) || !aligned(dx, size) || !aligned(dweight, 4) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  const int parts = parts_of(M, H);
+  const size_t need = (size_t)parts * H * 4;
+  if (workspace_bytes < need) return MOE_ERR_ARG;
+  const bool in_place = dsum == dx && (M <= 1 || ld_dsum == ld_dx);
+  if (any_overlap({{dx, rows_bytes(M, H, ld_dx, size)}, {dweight, (size_t)H * 4}, {workspace, need}},
+                  {{dy, rows_bytes(M, H, ld_dy, size)}, {r, rows_bytes(M, H, ld_r, size)},
+                   {weight, (size_t)H * dtype_size(weight_dtype)}, {rstd, (size_t)M * 4},
+                   {in_place ? nullptr : dsum, rows_bytes(M, H, ld_dsum, size)}}))
+    return MOE_ERR_ALIAS;
+  const moe::NormBackwardArgs a{ld_dy, ld_r, ld_dsum, ld_dx, rstd, static_cast<float*>(workspace), M, H};
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool f = weight_dtype == MOE_F32;
+  (void)hipGetLastError();
+  if (dtype == MOE_F32) moe_host::by_row(H, Backward<float, float>{st, dy, r, weight, dsum, dx, a, parts});
+  else if (dtype == MOE_BF16) launch<__bf16>(st, dy, r, weight, f, dsum, dx, a, parts);
+  else launch<moe::f16_t>(st, dy, r, weight, f, dsum, dx, a, parts);
+  hipLaunchKernelGGL(moe::rms_norm_weight_kernel, dim3((unsigned)((H + 31) / 32)), dim3(moe::kNormSumThreads), 0, st, a.part,
+                     dweight, parts, H);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+}  // extern "C"
