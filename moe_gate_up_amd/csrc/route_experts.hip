@@ -35,15 +35,21 @@ int check_route(int T, int E, int k) {
   return MOE_OK;
 }
 
+constexpr int kGrid = 1024;   // workgroups of a pass over many rows: 4 a CU, as many as stay at a time
+
 struct Choose {
   hipStream_t st;
   const void* logits;
   const moe::ScoreArgs& a;
   template <typename T, int LR, int V, int C>
   void operator()() const {
-    const int rows = moe::kScoreWaves * (64 / LR);
-    hipLaunchKernelGGL((moe::route_experts_kernel<T, LR, V, C>), dim3((unsigned)((a.T + rows - 1) / rows)),
-                       dim3(moe::kScoreThreads), 0, st, static_cast<const T*>(logits), a);
+    const int rows = moe::kScoreWaves * (64 / LR), n = (a.T + rows - 1) / rows;
+    const dim3 grid((unsigned)(n < kGrid ? n : kGrid)), block(moe::kScoreThreads);
+    const T* x = static_cast<const T*>(logits);
+    if (!a.bias) hipLaunchKernelGGL((moe::route_experts_kernel<T, LR, V, C, moe::kByLogit>), grid, block, 0, st, x, a);
+    else if (a.flags & moe::kScoreSigmoid)
+      hipLaunchKernelGGL((moe::route_experts_kernel<T, LR, V, C, moe::kBySigmoid>), grid, block, 0, st, x, a);
+    else hipLaunchKernelGGL((moe::route_experts_kernel<T, LR, V, C, moe::kBySoftmax>), grid, block, 0, st, x, a);
   }
 };
 template <typename T, int LR, int C, typename F>
@@ -146,6 +152,7 @@ int moe_decode_route_experts(const void* logits, long long ld, int dtype, const 
   const int lanes = E > 256 || k > 16 || groups > 16 ? 64 : 16, Eg = E / groups;
   int lg = 0;
   while ((2 << lg) * groups <= lanes) ++lg;
+  if (Eg == 1) flags &= ~MOE_ROUTE_GROUP_TOP2;         // the largest is all there is
   const bool whole = quads(logits, T, Eg, ld, dtype);
   const int c = whole ? 4 : 1, n = (Eg + (c << lg) - 1) / (c << lg) * c;
   const moe::ScoreArgs a{bias, topk_ids, topk_weights, ld, T, E, k, groups, Eg, top_groups, lg, flags, scale};
