@@ -524,7 +524,7 @@ int moe_decode_combine_backward(const void *dy, long long ld_dy, const void *row
  * of at least moe_decode_rms_norm_backward_workspace() bytes, 256-byte aligned, used
  * until the launches complete (calls that may overlap in time need one each); it need
  * not be cleared.
- * Limits: H <= 32768; M < 2^26 up to 4096 columns, 2^24 up to 16384, else 2^22;
+ * Limits: H <= 32768; M < 2^26 up to 1024 columns, 2^24 up to 16384, else 2^22;
  * strides up to 2^30.  M == 0 is a valid no-op that writes nothing. */
 int moe_decode_rms_norm(const void *x, long long ld_x, const void *residual, long long ld_residual, int dtype,
                         const void *weight, int weight_dtype, float eps, void *y, long long ld_y,

@@ -29,10 +29,9 @@ struct Layout {
   Layout(int M, int L) {
     if (M <= moe::kAdFew) return;
     auto take = [&](size_t b) { const size_t r = total; total += (b + 255) & ~(size_t)255; return r; };
-    const int parts = moe::sort_parts(M);
     order = take((size_t)M * 4);
     counts = take((size_t)(L + 1) * 4);
-    before = take(parts == 1 ? 0 : (size_t)parts * (L + 1) * 4);
+    before = take(moe::sort_counts(M, L + 1) * 4);
   }
 };
 
@@ -107,7 +106,7 @@ int moe_decode_adapters(const void* x, long long ld_x, int dtype, const int32_t*
   if (W.total) {
     const moe::SortArgs s{row_adapters, nullptr, counts, order, nullptr, reinterpret_cast<int32_t*>(ws + W.before), M, L + 1,
                           1, moe::sort_part(M), 0, true};
-    moe::launch_sort(st, s, moe::sort_parts(M));
+    moe::launch_sort(st, s);
   }
   const moe::AdapterArgs args{row_adapters, scaling, W.total ? order : nullptr, W.total ? counts : nullptr, ld_x, ld_base,
                               ld_y, M, K, N, R, L, 1, N};

@@ -127,11 +127,13 @@ __global__ __launch_bounds__(kAdThreads) void adapters_kernel(const T* __restric
       const long long r = rows[m];
       for (int c = c0 + tid * kPiece; c < c1; c += kAdThreads * kPiece) {
         Piece<T> p;
-        if (base) p.load(base + r * a.ld_base + c, c1 - c);
-        else
+        if (base) {
+          p.request(base + r * a.ld_base, c, a.N);
+          p.settle(c, a.N);
+        } else
 #pragma unroll
           for (int i = 0; i < 4 * Piece<T>::kWords; ++i) p.v[i] = 0;
-        p.store(y + r * a.ld_y + c, c1 - c);
+        p.store(y + r * a.ld_y, c, a.N);
       }
     }
     return;
@@ -222,12 +224,13 @@ __global__ __launch_bounds__(kAdThreads) void adapters_kernel(const T* __restric
     if (i16 >= n) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = n0 + 16 * q + 8 * h, left = c1 - c;
-      if (left <= 0) continue;
+      const int c = n0 + 16 * q + 8 * h;
+      if (c >= c1) continue;
       float f[kPiece];
       Piece<T> p;
       if (base) {
-        p.load(base + row * a.ld_base + c, left);
+        p.request(base + row * a.ld_base, c, a.N);
+        p.settle(c, a.N);
         p.values(f);
       }
 #pragma unroll
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(kAdThreads) void adapters_kernel(const T* __restric
         f[j] = base ? f[j] + d : d;
       }
       p.set(f);
-      p.store(y + row * a.ld_y + c, left);
+      p.store(y + row * a.ld_y, c, a.N);
     }
   }
 }

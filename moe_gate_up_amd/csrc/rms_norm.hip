@@ -15,6 +15,19 @@ using moe_host::rows_stride_ok;
 size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
 
+// f<WR, P>(): wavefronts of a row and pieces of a lane.  One wavefront for the shortest rows, which have no work for
+// more, four as soon as they do, sixteen where four lanes' registers do not hold the row.
+template <typename F>
+void by_row(int H, const F& f) {
+  if (H <= 512) f.template operator()<1, 1>();
+  else if (H <= 1024) f.template operator()<1, 2>();
+  else if (H <= 2048) f.template operator()<4, 1>();
+  else if (H <= 4096) f.template operator()<4, 2>();
+  else if (H <= 8192) f.template operator()<4, 4>();
+  else if (H <= 16384) f.template operator()<4, 8>();
+  else f.template operator()<16, 4>();
+}
+
 template <typename T, typename W>
 struct Norm {
   hipStream_t st;
@@ -32,8 +45,8 @@ struct Norm {
 template <typename T>
 void launch(hipStream_t st, const void* x, const void* res, const void* weight, bool f32_weight, void* y, void* sum,
             const moe::NormArgs& a) {
-  if (f32_weight) moe_host::by_row(a.H, Norm<T, float>{st, x, res, weight, y, sum, a});
-  else moe_host::by_row(a.H, Norm<T, T>{st, x, res, weight, y, sum, a});
+  if (f32_weight) by_row(a.H, Norm<T, float>{st, x, res, weight, y, sum, a});
+  else by_row(a.H, Norm<T, T>{st, x, res, weight, y, sum, a});
 }
 
 }  // namespace
@@ -68,7 +81,7 @@ extern "C" int moe_decode_rms_norm(const void* x, long long ld_x, const void* re
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const bool f = weight_dtype == MOE_F32;
   (void)hipGetLastError();
-  if (dtype == MOE_F32) moe_host::by_row(H, Norm<float, float>{st, x, residual, weight, y, sum, a});
+  if (dtype == MOE_F32) by_row(H, Norm<float, float>{st, x, residual, weight, y, sum, a});
   else if (dtype == MOE_BF16) launch<__bf16>(st, x, residual, weight, f, y, sum, a);
   else launch<moe::f16_t>(st, x, residual, weight, f, y, sum, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;

@@ -14,21 +14,19 @@ using moe_host::rows_stride_ok;
 size_t dtype_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
 
-constexpr int kParts = 512;   // workgroups, each with a row of the workspace
+int parts_of(int M) { return M < moe::kNormBackParts ? M : moe::kNormBackParts; }
 
-struct Parts {
-  int M;
-  int* parts;
-  template <int WR, int P>
-  void operator()() const {
-    const int n = (M + moe::norm_rows(WR) - 1) / moe::norm_rows(WR);
-    *parts = n < kParts ? n : kParts;
-  }
-};
-int parts_of(int M, int H) {
-  int n = 0;
-  moe_host::by_row(H, Parts{M, &n});
-  return n;
+// f<WR, P>(): wavefronts of a row and pieces of a lane, of which one leaves the registers for the next row's; the
+// longest rows spill some.
+template <typename F>
+void by_row(int H, const F& f) {
+  if (H <= 512) f.template operator()<1, 1>();
+  else if (H <= 1024) f.template operator()<2, 1>();
+  else if (H <= 2048) f.template operator()<4, 1>();
+  else if (H <= 4096) f.template operator()<8, 1>();
+  else if (H <= 8192) f.template operator()<16, 1>();
+  else if (H <= 16384) f.template operator()<16, 2>();
+  else f.template operator()<16, 4>();
 }
 
 template <typename T, typename W>
@@ -41,15 +39,15 @@ struct Backward {
   template <int WR, int P>
   void operator()() const {
     hipLaunchKernelGGL((moe::rms_norm_backward_kernel<T, W, WR, P>), dim3((unsigned)parts),
-                       dim3((unsigned)moe::norm_threads(WR)), 0, st, static_cast<const T*>(dy), static_cast<const T*>(r),
+                       dim3(moe::kNormBackThreads), 0, st, static_cast<const T*>(dy), static_cast<const T*>(r),
                        static_cast<const W*>(weight), static_cast<const T*>(dsum), static_cast<T*>(dx), a);
   }
 };
 template <typename T>
 void launch(hipStream_t st, const void* dy, const void* r, const void* weight, bool f32_weight, const void* dsum, void* dx,
             const moe::NormBackwardArgs& a, int parts) {
-  if (f32_weight) moe_host::by_row(a.H, Backward<T, float>{st, dy, r, weight, dsum, dx, a, parts});
-  else moe_host::by_row(a.H, Backward<T, T>{st, dy, r, weight, dsum, dx, a, parts});
+  if (f32_weight) by_row(a.H, Backward<T, float>{st, dy, r, weight, dsum, dx, a, parts});
+  else by_row(a.H, Backward<T, T>{st, dy, r, weight, dsum, dx, a, parts});
 }
 
 }  // namespace
@@ -60,7 +58,7 @@ int moe_decode_rms_norm_backward_workspace(int M, int H, size_t* bytes) {
   const int rc = moe_host::check_norm(M, H);
   if (rc) return rc;
   if (!bytes) return MOE_ERR_NULL;
-  *bytes = (size_t)parts_of(M, H) * H * 4;
+  *bytes = (size_t)parts_of(M) * H * 4;
   return MOE_OK;
 }
 
@@ -80,7 +78,7 @@ int moe_decode_rms_norm_backward(const void* dy, long long ld_dy, const void* r,
   if (!aligned(dy, size) || !aligned(r, size) || !aligned(weight, dtype_size(weight_dtype)) || !aligned(rstd, 4) ||
       !aligned(dsum, size) || !aligned(dx, size) || !aligned(dweight, 4) || !aligned(workspace, 256))
     return MOE_ERR_ALIGN;
-  const int parts = parts_of(M, H);
+  const int parts = parts_of(M);
   const size_t need = (size_t)parts * H * 4;
   if (workspace_bytes < need) return MOE_ERR_ARG;
   const bool in_place = dsum == dx && (M <= 1 || ld_dsum == ld_dx);
@@ -93,7 +91,7 @@ int moe_decode_rms_norm_backward(const void* dy, long long ld_dy, const void* r,
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const bool f = weight_dtype == MOE_F32;
   (void)hipGetLastError();
-  if (dtype == MOE_F32) moe_host::by_row(H, Backward<float, float>{st, dy, r, weight, dsum, dx, a, parts});
+  if (dtype == MOE_F32) by_row(H, Backward<float, float>{st, dy, r, weight, dsum, dx, a, parts});
   else if (dtype == MOE_BF16) launch<__bf16>(st, dy, r, weight, f, dsum, dx, a, parts);
   else launch<moe::f16_t>(st, dy, r, weight, f, dsum, dx, a, parts);
   hipLaunchKernelGGL(moe::rms_norm_weight_kernel, dim3((unsigned)((H + 31) / 32)), dim3(moe::kNormSumThreads), 0, st, a.part,

@@ -191,8 +191,7 @@ int moe_decode_sort_slots_workspace(int T, int E, int k, size_t* bytes) {
   const int rc = check_sort(T, E, k);
   if (rc) return rc;
   if (!bytes) return MOE_ERR_NULL;
-  const int parts = T ? moe::sort_parts(T * k) : 1;
-  *bytes = parts == 1 ? 0 : (size_t)parts * E * 4;
+  *bytes = T ? moe::sort_counts(T * k, E) * 4 : 0;
   return MOE_OK;
 }
 
@@ -201,9 +200,9 @@ int moe_decode_sort_slots(const int32_t* topk_ids, const uint8_t* valid, int32_t
   const int rc = check_sort(T, E, k);
   if (rc) return rc;
   if (T == 0) return MOE_OK;
-  const int slots = T * k, parts = moe::sort_parts(slots);
-  const size_t need = parts == 1 ? 0 : (size_t)parts * E * 4, slot_bytes = (size_t)slots * 4;
-  if (parts == 1) workspace = nullptr;
+  const int slots = T * k;
+  const size_t need = moe::sort_counts(slots, E) * 4, slot_bytes = (size_t)slots * 4;
+  if (!need) workspace = nullptr;
   if (!topk_ids || !counts || !x_rows || !positions || (need && !workspace)) return MOE_ERR_NULL;
   if (!aligned(topk_ids, 4) || !aligned(counts, 4) || !aligned(x_rows, 4) || !aligned(positions, 4) ||
       !aligned(workspace, 256))
@@ -216,7 +215,7 @@ int moe_decode_sort_slots(const int32_t* topk_ids, const uint8_t* valid, int32_t
   const moe::SortArgs a{topk_ids, valid, counts, x_rows, positions, static_cast<int32_t*>(workspace), slots, E, k,
                         moe::sort_part(slots), magic, false};
   (void)hipGetLastError();
-  moe::launch_sort(static_cast<hipStream_t>(stream), a, parts);
+  moe::launch_sort(static_cast<hipStream_t>(stream), a);
   return launched();
 }
 

@@ -1,12 +1,15 @@
 // Slots of tokens sorted by expert (the definition is at moe_decode_sort_slots in
 // include/moe_decode.h): a counting sort that keeps the slots' order.
 //
-// The slots are cut into parts of whole rounds of 64 for each wavefront.  A slot's
-// rank among those of its expert in its round comes from ballots, one for each bit
+// The slots are cut into parts of whole rounds of 64 for each of 16 wavefronts.  A
+// slot's rank among those of its expert in its round comes from ballots, one for each bit
 // of the expert's number; its place is that, plus the expert's slots in earlier
 // rounds, wavefronts and parts, plus the slots of earlier experts.
-// One part: one launch.  More: a first launch counts each part's slots of each
-// expert, and every part of the second adds up what lies before it.
+// Up to 8192 slots one launch does it: each part counts the slots of all others for
+// itself, which costs less than a launch.  Beyond, a first launch counts each part's slots
+// of each expert, and the parts of the second add up what lies before them.  Counts
+// are added in LDS by one lane for all of its round that share its expert: lanes of one
+// address are served one after another (32768 slots counted lane by lane 20 us).
 #pragma once
 
 #include "prims.hpp"
@@ -16,18 +19,20 @@ namespace moe {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortExperts = 1024;      // E limit
-constexpr int kSortAlone = 4096;        // slots that one workgroup takes without a second launch
+constexpr int kSortOnce = 8192;         // slots up to which one launch does it (their numbers fit in 16 bits)
 constexpr int kSortMostParts = 256;
 
 __host__ __device__ constexpr int sort_parts(int slots) {
-  if (slots <= kSortAlone) return 1;
-  const int n = (slots + 2 * kSortThreads - 1) / (2 * kSortThreads);
+  const int n = (slots - 1) / kSortThreads + 1;
   return n < kSortMostParts ? n : kSortMostParts;
+}
+// Integers of workspace for the parts' counts.
+__host__ __device__ constexpr size_t sort_counts(int slots, int E) {
+  return slots <= kSortOnce ? 0 : (size_t)sort_parts(slots) * E;
 }
 // Slots of one part: whole rounds of all wavefronts.
 __host__ __device__ constexpr int sort_part(int slots) {
-  const int parts = sort_parts(slots);
-  const int rounds = (slots - 1) / (parts * kSortThreads) + 1;
+  const int rounds = (slots - 1) / (sort_parts(slots) * kSortThreads) + 1;
   return rounds * kSortThreads;
 }
 
@@ -37,7 +42,7 @@ struct SortArgs {
   int32_t* counts;
   int32_t* x_rows;
   int32_t* positions;
-  int32_t* before;   // [parts, E] slots of each expert in each part
+  int32_t* before;   // [parts, E] slots of each expert in each part, where there are more than kSortOnce
   int slots, E, k, part;
   uint32_t magic;    // ceil(2^32 / k)
   bool rest;         // ids outside [0, E - 1) are of the last expert
@@ -57,64 +62,100 @@ __device__ __forceinline__ int sort_expert(const SortArgs& a, int s, int end) {
   return on ? e : -1;
 }
 
+// A round of 64 slots: the lanes that share this lane's expert (< 1 << bits).
+__device__ __forceinline__ uint64_t sort_peers(int e, int bits) {
+  uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t ones = __builtin_amdgcn_ballot_w64(e >> b & 1);
+    same &= e >> b & 1 ? ones : ~ones;
+  }
+  return same;
+}
+__device__ __forceinline__ int sort_bits(int E) { return E > 1 ? 32 - __builtin_clz(E - 1) : 0; }
+// One lane of them, the last.
+__device__ __forceinline__ bool sort_speaks(uint64_t same, int lane) { return same >> lane == 1; }
+
 static __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ int32_t hist[kSortExperts];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, bits = sort_bits(a.E);
   const int s0 = (int)blockIdx.x * a.part, s1 = min(a.slots - s0, a.part) + s0;
-  for (int e = tid; e < a.E; e += kSortThreads) hist[e] = 0;
+  if (tid < a.E) hist[tid] = 0;
+  int e = sort_expert(a, s0 + tid, s1);
   __syncthreads();
-  for (int s = s0 + tid; s < s1; s += kSortThreads) {
-    const int e = sort_expert(a, s, s1);
-    if (e >= 0) atomicAdd(&hist[e], 1);
+  for (int s = s0 + tid; s - lane < s1; s += kSortThreads) {   // whole wavefronts
+    const int next = sort_expert(a, s + kSortThreads, s1);
+    const uint64_t same = sort_peers(e, bits);
+    if (e >= 0 && sort_speaks(same, lane)) atomicAdd(&hist[e], __builtin_popcountll(same));
+    e = next;
   }
   __syncthreads();
-  for (int e = tid; e < a.E; e += kSortThreads) a.before[(size_t)blockIdx.x * a.E + e] = hist[e];
+  if (tid < a.E) a.before[(size_t)blockIdx.x * a.E + tid] = hist[tid];
 }
 
-// ALONE: there is no other part.
-template <bool ALONE>
+// ONCE: the parts count for themselves.  SINGLE: a wavefront has one round.
+template <bool ONCE, bool SINGLE>
 static __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ uint16_t wave_count[kSortWaves][kSortExperts];   // of the part: fewer than 2^16 in each wavefront's share
+  __shared__ uint32_t seen[kSortExperts];   // slots of an expert, and of them before this part: in ONCE's one word, or
+  __shared__ uint32_t seen_before[ONCE ? 1 : kSortExperts];   // in two
   __shared__ int32_t start[kSortExperts];   // where the part's slots of each expert begin
   __shared__ int32_t sums[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int s0 = (int)blockIdx.x * a.part, s1 = min(a.slots - s0, a.part) + s0;
   const int share = a.part / kSortWaves, w0 = s0 + w * share;   // this wavefront's slots
   const int w1 = min(w0 + share, s1);
-  for (int i = tid; i < kSortWaves * a.E; i += kSortThreads) wave_count[i / a.E][i % a.E] = 0;
-  int bits = 0;
-  while ((1 << bits) < a.E) ++bits;
+  const int mine_e = SINGLE ? sort_expert(a, w0 + lane, w1) : -1;
+  if (tid < a.E) {
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) wave_count[i][tid] = 0;
+    seen[tid] = 0;
+    if (!ONCE) seen_before[tid] = 0;
+  }
+  const int bits = sort_bits(a.E);
   __syncthreads();
 
-  // a round of 64 slots: the lanes that share this lane's expert
-  auto peers = [&](int e) {
-    uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t ones = __builtin_amdgcn_ballot_w64(e >> b & 1);
-      same &= e >> b & 1 ? ones : ~ones;
-    }
-    return same;
-  };
+  uint64_t mine_same = 0;
   for (int s = w0; s < w1; s += 64) {
-    const int e = sort_expert(a, s + lane, w1);
-    const uint64_t same = peers(e);
-    if (e >= 0 && (same >> lane) == 1) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);   // the last of them
+    const int e = SINGLE ? mine_e : sort_expert(a, s + lane, w1);
+    const uint64_t same = sort_peers(e, bits);
+    if (SINGLE) mine_same = same;
+    if (e >= 0 && sort_speaks(same, lane)) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);   // the last of them
   }
-  __syncthreads();
-  // experts' totals and what lies before this part; thread e holds expert e
-  int total = 0, mine = 0;
-  if (tid < a.E) {
-    if constexpr (ALONE) {
+  if constexpr (ONCE) {
+    for (int i0 = 0; i0 < a.slots; i0 += kSortOnce / 2) {
+      constexpr int U = kSortOnce / 2 / kSortThreads;   // requested together
+      int e[U];
 #pragma unroll
-      for (int i = 0; i < kSortWaves; ++i) total += wave_count[i][tid];
-    } else {
-      const int parts = (int)gridDim.x;
-      for (int i = 0; i < parts; ++i) {
-        const int n = a.before[(size_t)i * a.E + tid];
-        mine += i < (int)blockIdx.x ? n : 0;
-        total += n;
+      for (int u = 0; u < U; ++u) e[u] = sort_expert(a, i0 + u * kSortThreads + tid, a.slots);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint64_t same = sort_peers(e[u], bits);
+        const uint32_t n = (uint32_t)__builtin_popcountll(same);
+        // a round lies before this part or not as a whole
+        if (e[u] >= 0 && sort_speaks(same, lane)) atomicAdd(&seen[e[u]], n << 16 | (i0 + u * kSortThreads + tid < s0 ? n : 0u));
       }
     }
+  } else {
+    // 1024 threads share out the parts' counts: several threads an expert where there are fewer experts
+    const int stride = 1 << bits, first = tid >> bits, e = tid & (stride - 1);
+    uint32_t n = 0, before = 0;
+    if (e < a.E) {
+#pragma unroll 8
+      for (int i = first; i < (int)gridDim.x; i += kSortThreads >> bits) {
+        const uint32_t c = (uint32_t)a.before[(size_t)i * a.E + e];
+        n += c;
+        before += i < (int)blockIdx.x ? c : 0u;
+      }
+      atomicAdd(&seen[e], n);
+      atomicAdd(&seen_before[e], before);
+    }
+  }
+  __syncthreads();
+  // thread e holds expert e
+  int total = 0, mine = 0;
+  if (tid < a.E) {
+    total = (int)(ONCE ? seen[tid] >> 16 : seen[tid]);
+    mine = (int)(ONCE ? seen[tid] & 0xFFFFu : seen_before[tid]);
   }
   const int upto = wave_incl_scan(total);
   if (lane == 63) sums[w] = upto;
@@ -138,8 +179,8 @@ static __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArg
   }
   __syncthreads();
   for (int s = w0; s < w1; s += 64) {
-    const int e = sort_expert(a, s + lane, w1);
-    const uint64_t same = peers(e);
+    const int e = SINGLE ? mine_e : sort_expert(a, s + lane, w1);
+    const uint64_t same = SINGLE ? mine_same : sort_peers(e, bits);
     if (s + lane < w1) {
       int at = -1;
       if (e >= 0) {
@@ -148,22 +189,25 @@ static __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArg
       }
       if (a.positions) a.positions[s + lane] = at;
     }
-    __builtin_amdgcn_wave_barrier();   // all have read before the last of them adds
-    if (e >= 0 && (same >> lane) == 1) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);
-    __builtin_amdgcn_wave_barrier();
+    if (!SINGLE) {
+      __builtin_amdgcn_wave_barrier();   // all have read before the last of them adds
+      if (e >= 0 && sort_speaks(same, lane)) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);
+      __builtin_amdgcn_wave_barrier();
+    }
   }
   for (int s = max(s0, all) + tid; s < s1; s += kSortThreads) a.x_rows[s] = -1;   // behind the last expert's
 }
 
-// Both launches (or the one), of `parts` workgroups.
-inline void launch_sort(hipStream_t st, const SortArgs& a, int parts) {
-  const dim3 grid((unsigned)parts), block(kSortThreads);
-  if (parts == 1) {
-    hipLaunchKernelGGL(sort_place_kernel<true>, grid, block, 0, st, a);
-  } else {
-    hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, st, a);
-    hipLaunchKernelGGL(sort_place_kernel<false>, grid, block, 0, st, a);
+// The one launch, or both.
+inline void launch_sort(hipStream_t st, const SortArgs& a) {
+  const dim3 grid((unsigned)sort_parts(a.slots)), block(kSortThreads);
+  if (a.slots <= kSortOnce) {
+    hipLaunchKernelGGL((sort_place_kernel<true, true>), grid, block, 0, st, a);
+    return;
   }
+  hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, st, a);
+  if (a.part == kSortThreads) hipLaunchKernelGGL((sort_place_kernel<false, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((sort_place_kernel<false, false>), grid, block, 0, st, a);
 }
 
 }  // namespace moe

@@ -34,7 +34,7 @@ def route_backward(logits=at(0), ld=128, dtype=mg.MOE_F32, ids=at(1), grad=at(2)
     return mg.lib().moe_decode_route_experts_backward(P(logits), ld, dtype, P(ids), P(grad), P(d), ld_d, T, E, k, flags, 1.0, None)
 
 
-def sort(ids=at(0), valid=0, counts=at(1), rows=at(2), pos=at(3), ws=at(4), ws_bytes=None, T=4096, E=128, k=8):
+def sort(ids=at(0), valid=0, counts=at(1), rows=at(2), pos=at(3), ws=at(4), ws_bytes=None, T=8192, E=128, k=8):
     if ws_bytes is None:
         ws_bytes = size_of(mg.lib().moe_decode_sort_slots_workspace, T, E, k)
     return mg.lib().moe_decode_sort_slots(P(ids), P(valid), P(counts), P(rows), P(pos), P(ws), ws_bytes, T, E, k, None)
@@ -172,7 +172,7 @@ def test_empty_calls_do_nothing():
 
 
 def test_workspaces():
-    assert mg.moe_decode_sort_slots_workspace(512, 1024, 8) == 0 < mg.moe_decode_sort_slots_workspace(513, 1024, 8)
+    assert mg.moe_decode_sort_slots_workspace(1024, 1024, 8) == 0 < mg.moe_decode_sort_slots_workspace(1025, 1024, 8)
     assert mg.moe_decode_adapters_workspace(512, 64, 64, 8, 4) == 0 < mg.moe_decode_adapters_workspace(513, 64, 64, 8, 4)
     assert mg.moe_decode_rms_norm_backward_workspace(1, 100) >= 400
     for fn, args in ((mg.moe_decode_sort_slots_workspace, (1 << 24, 8, 1)), (mg.moe_decode_adapters_workspace, (1, 4, 1, 8, 1)),

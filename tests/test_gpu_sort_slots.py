@@ -44,7 +44,7 @@ def check(ids, valid, E):
 
 
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 8, 128), (3, 5, 7), (32, 8, 128), (63, 1, 1024), (64, 1, 2), (65, 3, 1000), (512, 8, 64),
-                                   (513, 8, 64), (4096, 1, 3), (4097, 1, 1), (1000, 8, 128), (4096, 8, 128), (10533, 6, 100), (20000, 64, 1024),
+                                   (513, 8, 64), (4096, 1, 3), (4097, 1, 1), (1000, 8, 128), (4096, 8, 128), (4095, 8, 1024), (1024, 8, 128), (8193, 1, 77), (4097, 8, 128), (32768, 1, 1000), (32769, 1, 1024), (262144, 1, 100), (262145, 1, 100), (10533, 6, 100), (20000, 64, 1024),
                                    (70001, 7, 1023), (300000, 8, 256), (16777215, 1, 16)], ids=str)
 def test_sorted(dev, shape):
     T, k, E = shape
@@ -71,11 +71,11 @@ def test_one_expert_none_and_all(dev, T):
 
 
 def test_graph_stream_workspace(dev):
-    T, k, E = 3000, 8, 128
+    T, k, E = 5000, 8, 128
     g = torch.Generator().manual_seed(1)
     ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).to(dev)
     need = mg.moe_decode_sort_slots_workspace(T, E, k)
-    assert need > 0 == mg.moe_decode_sort_slots_workspace(512, E, k)
+    assert need > 0 == mg.moe_decode_sort_slots_workspace(1024, E, k)
     ws = torch.full((need,), 0xAB, dtype=torch.uint8, device=dev)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
