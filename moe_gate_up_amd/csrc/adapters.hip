@@ -23,43 +23,67 @@ int check(int M, int K, int N, int R, int L) {
   return MOE_OK;
 }
 
-// Workspace of the sort: the rows by adapter, their numbers, and the parts'.
+int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : R <= 128 ? 8 : 16; }
+bool few(int M) { return M <= moe::kAdFew; }
+// At most: full units, and one that is not for each adapter and for none.
+long long units_of(int M, int L, int rows) { return M / rows + (L + 1 < M ? L + 1 : M); }
+// Shares of K: enough workgroups for the chip, each of what it takes at a time at least.
+int shares_of(int M, int K, int R, int L) {
+  const long long units = units_of(M, L, moe::kAdInner), want = (kTargetWorkgroups / 2 + units - 1) / units;
+  const int most = (K + moe::ad_span(rank_tiles(R)) - 1) / moe::ad_span(rank_tiles(R));
+  return (int)(want < most ? want : most);
+}
+
+// Workspace of many rows: their order by adapter, the adapters' numbers of rows, the sort's parts' and v.
 struct Layout {
-  size_t order = 0, counts = 0, before = 0, total = 0;
-  Layout(int M, int L) {
-    if (M <= moe::kAdFew) return;
+  size_t order = 0, counts = 0, before = 0, v = 0, total = 0;
+  Layout(int M, int K, int R, int L) {
+    if (few(M)) return;
     auto take = [&](size_t b) { const size_t r = total; total += (b + 255) & ~(size_t)255; return r; };
     order = take((size_t)M * 4);
     counts = take((size_t)(L + 1) * 4);
     before = take(moe::sort_counts(M, L + 1) * 4);
+    v = take((size_t)shares_of(M, K, R, L) * M * rank_tiles(R) * 64);
   }
 };
 
 template <typename T, int RT>
 void go(hipStream_t st, const void* x, const void* A, const void* B, const void* base, void* y, moe::AdapterArgs a) {
-  const bool sorted = a.M > moe::kAdFew;
-  const long long units = sorted ? a.M / moe::kAdRows + (a.L + 1 < a.M ? a.L + 1 : a.M) : a.M;
-  // enough workgroups for the chip; each of them repeats the first product
-  const int groups = (a.N + moe::kAdCols - 1) / moe::kAdCols;
-  long long s = (kTargetWorkgroups + units - 1) / units;
-  const long long most = (groups + moe::kAdWaves - 1) / moe::kAdWaves;
-  s = s < 1 ? 1 : s > most ? most : s;
-  a.cols = (int)((groups + s - 1) / s) * moe::kAdCols;
-  a.splits = (a.N + a.cols - 1) / a.cols;
-  const dim3 grid((unsigned)(units * a.splits)), block(moe::kAdThreads);
   const T *px = static_cast<const T*>(x), *pa = static_cast<const T*>(A), *pb = static_cast<const T*>(B),
           *pbase = static_cast<const T*>(base);
-  if (sorted) hipLaunchKernelGGL((moe::adapters_kernel<T, RT, true>), grid, block, 0, st, px, pa, pb, pbase, static_cast<T*>(y), a);
-  else hipLaunchKernelGGL((moe::adapters_kernel<T, RT, false>), grid, block, 0, st, px, pa, pb, pbase, static_cast<T*>(y), a);
+  T* py = static_cast<T*>(y);
+  const long long units = few(a.M) ? a.M : units_of(a.M, a.L, moe::kAdOuter);
+  const int waves = few(a.M) ? moe::ad_waves(RT) : moe::kAdOuterThreads / 64;
+  const int target = few(a.M) ? kTargetWorkgroups / 2 : 2 * kTargetWorkgroups;
+  // ranges of columns: enough workgroups for the chip, of work for all their wavefronts
+  const int groups = (a.N + moe::kAdCols - 1) / moe::kAdCols;
+  long long s = (target + units - 1) / units;
+  const long long most = (groups + waves - 1) / waves;
+  s = s > most ? most : s;
+  a.cols = (int)((groups + s - 1) / s) * moe::kAdCols;
+  a.splits = (a.N + a.cols - 1) / a.cols;
+  if (few(a.M)) {
+    hipLaunchKernelGGL((moe::adapters_few_kernel<T, RT>), dim3((unsigned)(units * a.splits)), dim3(64 * moe::ad_waves(RT)), 0, st,
+                       px, pa, pb, pbase, py, a);
+    return;
+  }
+  a.shares = shares_of(a.M, a.K, a.R, a.L);
+  a.span = ((a.K + a.shares - 1) / a.shares + moe::kAdStep - 1) / moe::kAdStep * moe::kAdStep;
+  hipLaunchKernelGGL((moe::adapters_inner_kernel<T, RT>), dim3((unsigned)(units_of(a.M, a.L, moe::kAdInner) * a.shares)),
+                     dim3(4 * moe::kAdInner), 0, st, px, pa, a);
+  hipLaunchKernelGGL((moe::adapters_outer_kernel<T, RT>), dim3((unsigned)(units * a.splits)), dim3(moe::kAdOuterThreads), 0, st, pb,
+                     pbase, py, a);
 }
 template <typename T>
 void by_rank(hipStream_t st, const void* x, const void* A, const void* B, const void* base, void* y,
              const moe::AdapterArgs& a) {
-  if (a.R <= 16) go<T, 1>(st, x, A, B, base, y, a);
-  else if (a.R <= 32) go<T, 2>(st, x, A, B, base, y, a);
-  else if (a.R <= 64) go<T, 4>(st, x, A, B, base, y, a);
-  else if (a.R <= 128) go<T, 8>(st, x, A, B, base, y, a);
-  else go<T, 16>(st, x, A, B, base, y, a);
+  switch (rank_tiles(a.R)) {
+    case 1: return go<T, 1>(st, x, A, B, base, y, a);
+    case 2: return go<T, 2>(st, x, A, B, base, y, a);
+    case 4: return go<T, 4>(st, x, A, B, base, y, a);
+    case 8: return go<T, 8>(st, x, A, B, base, y, a);
+    default: return go<T, 16>(st, x, A, B, base, y, a);
+  }
 }
 
 }  // namespace
@@ -70,7 +94,7 @@ int moe_decode_adapters_workspace(int M, int K, int N, int R, int L, size_t* byt
   const int rc = check(M, K, N, R, L);
   if (rc) return rc;
   if (!bytes) return MOE_ERR_NULL;
-  *bytes = Layout(M, L).total;
+  *bytes = Layout(M, K, R, L).total;
   return MOE_OK;
 }
 
@@ -84,7 +108,7 @@ int moe_decode_adapters(const void* x, long long ld_x, int dtype, const int32_t*
   if (!rows_stride_ok(M, K, ld_x) || (M > 1 && ld_x % 8) || (base && !rows_stride_ok(M, N, ld_base)) ||
       !rows_stride_ok(M, N, ld_y))
     return MOE_ERR_SHAPE;
-  const Layout W(M, L);
+  const Layout W(M, K, R, L);
   if (!W.total) workspace = nullptr;
   if (!x || !row_adapters || !a || !b || !scaling || !y || (W.total && !workspace)) return MOE_ERR_NULL;
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 2) || !aligned(y, 2) ||
@@ -108,8 +132,8 @@ int moe_decode_adapters(const void* x, long long ld_x, int dtype, const int32_t*
                           1, moe::sort_part(M), 0, true};
     moe::launch_sort(st, s);
   }
-  const moe::AdapterArgs args{row_adapters, scaling, W.total ? order : nullptr, W.total ? counts : nullptr, ld_x, ld_base,
-                              ld_y, M, K, N, R, L, 1, N};
+  const moe::AdapterArgs args{row_adapters, scaling, order, counts, reinterpret_cast<float*>(ws + W.v), ld_x, ld_base, ld_y,
+                              M, K, N, R, L, 1, N, 1, K};
   if (dtype == MOE_BF16) by_rank<__bf16>(st, x, a, b, base, y, args);
   else by_rank<moe::f16_t>(st, x, a, b, base, y, args);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;

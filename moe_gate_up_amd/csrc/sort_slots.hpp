@@ -53,18 +53,20 @@ __device__ __forceinline__ int sort_token(const SortArgs& a, int s) {
   const int q = (int)__umulhi((uint32_t)s, a.magic);   // the quotient, or one more
   return q - (q * a.k > s ? 1 : 0);
 }
-// The expert of slot s; -1 where it is not counted.
+// The expert of slot s; -1 where it is not counted.  The loads are always made, of a slot that is there: one under a
+// condition of the lane's would be waited for at its end.
 __device__ __forceinline__ int sort_expert(const SortArgs& a, int s, int end) {
-  if (s >= end) return -1;
-  const int e = a.ids[s];
-  if (a.rest) return (unsigned)e < (unsigned)(a.E - 1) ? e : a.E - 1;
-  const bool on = (unsigned)e < (unsigned)a.E && (!a.valid || a.valid[sort_token(a, s)]);
-  return on ? e : -1;
+  const int from = min(s, a.slots - 1), e = a.ids[from];
+  if (a.rest) return s >= end ? -1 : (unsigned)e < (unsigned)(a.E - 1) ? e : a.E - 1;
+  const bool on = !a.valid || a.valid[sort_token(a, from)] != 0;
+  return (on & (s < end) & ((unsigned)e < (unsigned)a.E)) ? e : -1;
 }
 
 // A round of 64 slots: the lanes that share this lane's expert (< 1 << bits).
 __device__ __forceinline__ uint64_t sort_peers(int e, int bits) {
   uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
+  // all of one: rows of a prompt
+  if (__builtin_amdgcn_ballot_w64(e == __builtin_amdgcn_readfirstlane(e)) == ~0ull) return same;
   for (int b = 0; b < bits; ++b) {
     const uint64_t ones = __builtin_amdgcn_ballot_w64(e >> b & 1);
     same &= e >> b & 1 ? ones : ~ones;
@@ -104,7 +106,14 @@ static __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArg
   const int s0 = (int)blockIdx.x * a.part, s1 = min(a.slots - s0, a.part) + s0;
   const int share = a.part / kSortWaves, w0 = s0 + w * share;   // this wavefront's slots
   const int w1 = min(w0 + share, s1);
-  const int mine_e = SINGLE ? sort_expert(a, w0 + lane, w1) : -1;
+  constexpr int U = ONCE ? kSortOnce / kSortThreads : 1;   // the parts; ONCE: a slot of each, requested together
+  int parts_e[U], mine_e = -1;
+  if constexpr (ONCE) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) parts_e[u] = sort_expert(a, u * kSortThreads + tid, a.slots);
+  } else if constexpr (SINGLE) {
+    mine_e = sort_expert(a, w0 + lane, w1);
+  }
   if (tid < a.E) {
 #pragma unroll
     for (int i = 0; i < kSortWaves; ++i) wave_count[i][tid] = 0;
@@ -115,27 +124,29 @@ static __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArg
   __syncthreads();
 
   uint64_t mine_same = 0;
-  for (int s = w0; s < w1; s += 64) {
-    const int e = SINGLE ? mine_e : sort_expert(a, s + lane, w1);
-    const uint64_t same = sort_peers(e, bits);
-    if (SINGLE) mine_same = same;
-    if (e >= 0 && sort_speaks(same, lane)) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);   // the last of them
-  }
   if constexpr (ONCE) {
-    for (int i0 = 0; i0 < a.slots; i0 += kSortOnce / 2) {
-      constexpr int U = kSortOnce / 2 / kSortThreads;   // requested together
-      int e[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) e[u] = sort_expert(a, i0 + u * kSortThreads + tid, a.slots);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint64_t same = sort_peers(e[u], bits);
-        const uint32_t n = (uint32_t)__builtin_popcountll(same);
-        // a round lies before this part or not as a whole
-        if (e[u] >= 0 && sort_speaks(same, lane)) atomicAdd(&seen[e[u]], n << 16 | (i0 + u * kSortThreads + tid < s0 ? n : 0u));
+    for (int u = 0; u < U; ++u) {
+      if (u * kSortThreads >= a.slots) break;
+      const int e = parts_e[u];
+      const uint64_t same = sort_peers(e, bits);
+      const uint32_t n = (uint32_t)__builtin_popcountll(same);
+      if (e >= 0 && sort_speaks(same, lane)) {
+        atomicAdd(&seen[e], n << 16 | (u < (int)blockIdx.x ? n : 0u));
+        if (u == (int)blockIdx.x) wave_count[w][e] = (uint16_t)n;
+      }
+      if (u == (int)blockIdx.x) {
+        mine_e = e;
+        mine_same = same;
       }
     }
   } else {
+    for (int s = w0; s < w1; s += 64) {
+      const int e = SINGLE ? mine_e : sort_expert(a, s + lane, w1);
+      const uint64_t same = sort_peers(e, bits);
+      if (SINGLE) mine_same = same;
+      if (e >= 0 && sort_speaks(same, lane)) wave_count[w][e] += (uint16_t)__builtin_popcountll(same);
+    }
     // 1024 threads share out the parts' counts: several threads an expert where there are fewer experts
     const int stride = 1 << bits, first = tid >> bits, e = tid & (stride - 1);
     uint32_t n = 0, before = 0;
