@@ -223,7 +223,8 @@ __global__ __launch_bounds__(64 * ad_waves(RT)) void adapters_few_kernel(const T
       if (c >= c1) continue;
       float f[kPiece];
       if (base) {
-        p[h].settle(c, a.N);
+        if (base == y) p[h].settle_own(base + row * a.ld_base, c, a.N);
+        else p[h].settle(c, a.N);
         p[h].values(f);
       }
 #pragma unroll
@@ -489,7 +490,8 @@ __global__ __launch_bounds__(kAdOuterThreads) void adapters_outer_kernel(const T
         const float back = factor[m];
         float g[kPiece];
         if (base) {
-          p[i].settle(n0 + col, a.N);
+          if (base == y) p[i].settle_own(base + row[i] * a.ld_base, n0 + col, a.N);
+          else p[i].settle(n0 + col, a.N);
           p[i].values(g);
         }
 #pragma unroll

@@ -68,7 +68,8 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const T* __res
   }
   if (add) {
     float f[kPiece];
-    base.settle(c, a.N);
+    if (add == y) base.settle_own(add + (long long)t * a.ld_add, c, a.N);
+    else base.settle(c, a.N);
     base.values(f);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) sum[i] += f[i];

@@ -63,6 +63,15 @@ struct Piece {
       }
     }
   }
+  // settle() for a row that is written in place: another lane may have stored the elements in front of a short piece
+  // between its request and here, so the lane's own are read once more.
+  __device__ __forceinline__ void settle_own(const T* row, int c, int n) {
+    if (c + kPiece <= n || n < kPiece) return;
+    T t[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) t[i] = c + i < n ? row[c + i] : (T)0.0f;
+    __builtin_memcpy(v, t, sizeof(v));
+  }
   __device__ __forceinline__ void store(T* row, int c, int n) const { put<false>(row, c, n); }
   // As store(), past the caches: for results much larger than they are, which would push out what is still to be read.
   __device__ __forceinline__ void stream(T* row, int c, int n) const { put<true>(row, c, n); }

@@ -3,8 +3,8 @@ in float64.
 
 Tolerances, u = 2^-24.  A sum of n products in FP32, in any order, is within n u of the
 sum of their magnitudes: v = A x within K u sum |a x|.  v enters the second product as
-two 16-bit numbers, within 2^-18 of itself in bf16 (half a step of 2^-9 of a rest that is
-2^-9 of it); in FP16, scaled to the row's largest, within 2^-22 of itself and 2^-38 of
+two 16-bit numbers, within 2^-16 of itself in bf16 (half a step, 2^-8, of a rest that is at
+most half a step, 2^-8, of it); in FP16, scaled to the row's largest, within 2^-22 of itself and 2^-38 of
 the row's largest.  The second sum has 2 R products: (2 R + 8) u with the factor; base and
 result cost 2 u and one rounding to the type.
 """
@@ -50,7 +50,7 @@ def check(x, ids, a, b, s, base, y):
         m = (at == l).nonzero().flatten()
         X, A, B, f = x[m].double(), a[l].double(), b[l].double(), float(s[l].double())
         v = X @ A.t().contiguous()
-        ev = K * U * (X.abs() @ A.abs().t().contiguous()) + (2.0 ** -18 + (2 * R + 8) * U) * v.abs()
+        ev = K * U * (X.abs() @ A.abs().t().contiguous()) + (2.0 ** -16 + (2 * R + 8) * U) * v.abs()
         ev = ev + 2.0 ** -38 * v.abs().amax(1, keepdim=True)
         Bt = B.t().contiguous()
         ref = full[m] + f * (v @ Bt)
@@ -164,6 +164,15 @@ def test_graph_stream_workspace_and_repeat(dev):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("N", [5, 9, 65, 129, 257, 1030])
+def test_in_place_where_the_last_columns_are_another_wavefronts(dev, N):
+    for M in (100, 2000):
+        x, ids, a, b, s, base = make(N, M, 64, N, 16, 5, torch.bfloat16, dev)
+        y = run(x, ids, a, b, s, base)
+        mg.moe_decode_adapters(x, ids, a, b, s, base, base=base)
+        assert torch.equal(base, y)
 
 
 def test_refusals(dev):

@@ -176,6 +176,16 @@ def test_graph_and_repeat(dev):
         assert all(torch.equal(a, b) for a, b in zip(out, (y, dr, dw)))
 
 
+@pytest.mark.parametrize("N", [5, 9, 513, 1025, 2049, 4103])
+def test_in_place_where_the_last_columns_are_another_wavefronts(dev, N):
+    for dtype in (torch.bfloat16, torch.float32):
+        (rows, at, w, add, dy), _ = make(N, 300, 3, N, dtype, dev)
+        y = torch.empty_like(add)
+        mg.moe_decode_combine(rows, at, w, y, add=add)
+        mg.moe_decode_combine(rows, at, w, add, add=add)
+        assert torch.equal(add, y)
+
+
 def test_refusals(dev):
     (rows, at, w, add, dy), _ = make(13, 6, 4, 64, torch.bfloat16, dev)
     y = torch.empty_like(add)

@@ -246,6 +246,22 @@ def test_graph_stream_and_repeat(dev):
         assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
+@pytest.mark.parametrize("H", [5, 9, 513, 1025, 1031, 1537, 2049, 4097, 6145, 8193, 16385])
+def test_in_place_where_the_last_columns_are_another_wavefronts(dev, H):
+    """The last columns, fewer than 8, begin where a wavefront's share ends: the sum onto the residual and dx onto dsum
+    are as out of place."""
+    for dtype in (torch.bfloat16, torch.float32):
+        M = 600
+        x, res, w = make(H, M, H, dtype, dtype, dev)
+        y, total, _, _, rstd = forward(x, res, w, q=False)
+        dy = torch.randn(M, H, generator=torch.Generator().manual_seed(H)).to(dtype).to(dev)
+        dx, dw = backward(dy, total, w, rstd, res)
+        r2, y2, s2, dw2 = res.clone(), torch.empty_like(y), res.clone(), torch.empty_like(dw)
+        mg.moe_decode_rms_norm(x, w, EPS, y=y2, residual=r2, sum_out=r2)
+        mg.moe_decode_rms_norm_backward(dy, total, w, rstd, s2, dw2, dsum=s2)
+        assert torch.equal(r2, total) and torch.equal(y2, y) and torch.equal(s2, dx) and torch.equal(dw2, dw)
+
+
 def test_refusals(dev):
     x, res, w = make(8, 6, 64, torch.bfloat16, torch.bfloat16, dev)
     y, q, s = torch.empty_like(x), torch.empty(6, 64, dtype=torch.uint8, device=dev), torch.empty(6, 1, device=dev)
