@@ -368,6 +368,17 @@ def _rows(t, name, device, rows, cols):
     return ld
 
 
+def _mat(t, name, device, like, rows, cols):
+    """Address and row stride of a GPU matrix of the type of `like`, as _rows() checks it, in few lookups."""
+    if t.dtype is not like and _codes.get(t.dtype) != _codes[like]:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {like}")
+    if t.shape == (rows, cols) and t.get_device() == device:
+        ld, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), ld if rows > 1 else cols
+    return t.data_ptr(), _rows(t, name, device, rows, cols)
+
+
 def _flat(t, name, device, size, dtype):
     """Address of a contiguous GPU tensor of that shape (a tuple), or of that many elements (a number) where its rows
     have one meaning only."""
@@ -604,14 +615,12 @@ def moe_decode_combine(rows, positions, weights, y, add=None, stream=None):
     d = _gpu(rows, "rows")
     M, N = rows.shape
     T, k = positions.shape
+    t = rows.dtype
     dt = _dtype_code(rows, "rows", (MOE_F32, MOE_BF16, MOE_F16))
-    if _codes.get(y.dtype) != dt or (add is not None and _codes.get(add.dtype) != dt):
-        raise ValueError("y and add must have the type of rows")
-    _call("moe_decode_combine", L.moe_decode_combine, d, stream, rows.data_ptr(), _rows(rows, "rows", d, M, N), dt,
+    _call("moe_decode_combine", L.moe_decode_combine, d, stream, *_mat(rows, "rows", d, t, M, N), dt,
           _flat(positions, "positions", d, (T, k), _i32),
           None if weights is None else _flat(weights, "weights", d, (T, k), _f32),
-          None if add is None else add.data_ptr(), 0 if add is None else _rows(add, "add", d, T, N),
-          y.data_ptr(), _rows(y, "y", d, T, N), M, T, N, k)
+          *((None, 0) if add is None else _mat(add, "add", d, t, T, N)), *_mat(y, "y", d, t, T, N), M, T, N, k)
     return y
 
 
@@ -622,16 +631,13 @@ def moe_decode_combine_backward(dy, rows, positions, weights, drows, dweights, s
     d = _gpu(dy, "dy")
     T, N = dy.shape
     M, k = drows.shape[0], positions.shape[-1]
+    t = dy.dtype
     dt = _dtype_code(dy, "dy", (MOE_F32, MOE_BF16, MOE_F16))
     if dweights is not None and rows is None:
         raise ValueError("dweights need rows")
-    if _codes.get(drows.dtype) != dt or (rows is not None and _codes.get(rows.dtype) != dt):
-        raise ValueError("rows and drows must have the type of dy")
-    _call("moe_decode_combine_backward", L.moe_decode_combine_backward, d, stream, dy.data_ptr(), _rows(dy, "dy", d, T, N),
-          None if rows is None else rows.data_ptr(), 0 if rows is None else _rows(rows, "rows", d, M, N), dt,
-          _flat(positions, "positions", d, (T, k), _i32),
-          None if weights is None else _flat(weights, "weights", d, (T, k), _f32),
-          drows.data_ptr(), _rows(drows, "drows", d, M, N),
+    _call("moe_decode_combine_backward", L.moe_decode_combine_backward, d, stream, *_mat(dy, "dy", d, t, T, N),
+          *((None, 0) if rows is None else _mat(rows, "rows", d, t, M, N)), dt, _flat(positions, "positions", d, (T, k), _i32),
+          None if weights is None else _flat(weights, "weights", d, (T, k), _f32), *_mat(drows, "drows", d, t, M, N),
           None if dweights is None else _flat(dweights, "dweights", d, (T, k), _f32), M, T, N, k)
     return drows, dweights
 
@@ -644,20 +650,17 @@ def moe_decode_rms_norm(x, weight, eps, y=None, q=None, scales=None, residual=No
     L = _load()
     d = _gpu(x, "x")
     M, H = x.shape
+    t = x.dtype
     dt = _dtype_code(x, "x", (MOE_F32, MOE_BF16, MOE_F16))
-    p = [x.data_ptr(), _rows(x, "x", d, M, H)]
-    for t, name in ((residual, "residual"), (y, "y"), (sum_out, "sum_out")):
-        if t is None:
-            p += [None, 0]
-        else:
-            if _codes.get(t.dtype) != dt:
-                raise ValueError(f"{name} must have the type of x")
-            p += [t.data_ptr(), _rows(t, name, d, M, H)]
-    wt = _dtype_code(weight, "weight", (MOE_F32, dt))
-    _call("moe_decode_rms_norm", L.moe_decode_rms_norm, d, stream, *p[:4], dt, _flat(weight, "weight", d, H, weight.dtype),
-          wt, eps, *p[4:6], None if q is None else _flat(q, "q", d, (M, H), _u8),
-          None if scales is None else _flat(scales, "scales", d, (M, -(-H // 128)), _f32), *p[6:],
-          None if rstd is None else _flat(rstd, "rstd", d, M, _f32), M, H, MOE_QUANT_POW2 if pow2 else 0)
+    xp, xl = _mat(x, "x", d, t, M, H)
+    rp, rl = (None, 0) if residual is None else _mat(residual, "residual", d, t, M, H)
+    yp, yl = (None, 0) if y is None else _mat(y, "y", d, t, M, H)
+    sp, sl = (None, 0) if sum_out is None else _mat(sum_out, "sum_out", d, t, M, H)
+    _call("moe_decode_rms_norm", L.moe_decode_rms_norm, d, stream, xp, xl, rp, rl, dt,
+          _flat(weight, "weight", d, (H,), weight.dtype), dt if weight.dtype is t else _dtype_code(weight, "weight", (MOE_F32, dt)),
+          eps, yp, yl, None if q is None else _flat(q, "q", d, (M, H), _u8),
+          None if scales is None else _flat(scales, "scales", d, (M, -(-H // 128)), _f32), sp, sl,
+          None if rstd is None else _flat(rstd, "rstd", d, (M,), _f32), M, H, MOE_QUANT_POW2 if pow2 else 0)
 
 
 @functools.lru_cache(maxsize=256)
@@ -679,18 +682,17 @@ def moe_decode_rms_norm_backward(dy, r, weight, rstd, dx, dweight, dsum=None, wo
     L = _load()
     d = _gpu(dy, "dy")
     M, H = dy.shape
+    t = dy.dtype
     dt = _dtype_code(dy, "dy", (MOE_F32, MOE_BF16, MOE_F16))
-    for t, name in ((r, "r"), (dx, "dx"), (dsum, "dsum")):
-        if t is not None and _codes.get(t.dtype) != dt:
-            raise ValueError(f"{name} must have the type of dy")
+    gp, gl = _mat(dy, "dy", d, t, M, H)
+    rp, rl = _mat(r, "r", d, t, M, H)
+    sp, sl = (None, 0) if dsum is None else _mat(dsum, "dsum", d, t, M, H)
+    xp, xl = _mat(dx, "dx", d, t, M, H)
     ws, n, keep = _workspace(workspace, moe_decode_rms_norm_backward_workspace(M, H) if M else 0, d, stream,
                              "moe_decode_rms_norm_backward")
-    _call("moe_decode_rms_norm_backward", L.moe_decode_rms_norm_backward, d, stream, dy.data_ptr(),
-          _rows(dy, "dy", d, M, H), r.data_ptr(), _rows(r, "r", d, M, H), dt,
-          _flat(weight, "weight", d, H, weight.dtype), _dtype_code(weight, "weight", (MOE_F32, dt)),
-          _flat(rstd, "rstd", d, M, _f32), None if dsum is None else dsum.data_ptr(),
-          0 if dsum is None else _rows(dsum, "dsum", d, M, H), dx.data_ptr(), _rows(dx, "dx", d, M, H),
-          _flat(dweight, "dweight", d, H, _f32), ws, n, M, H)
+    _call("moe_decode_rms_norm_backward", L.moe_decode_rms_norm_backward, d, stream, gp, gl, rp, rl, dt,
+          _flat(weight, "weight", d, (H,), weight.dtype), dt if weight.dtype is t else _dtype_code(weight, "weight", (MOE_F32, dt)),
+          _flat(rstd, "rstd", d, (M,), _f32), sp, sl, xp, xl, _flat(dweight, "dweight", d, (H,), _f32), ws, n, M, H)
     return dx, dweight
 
 
@@ -713,18 +715,20 @@ def moe_decode_adapters(x, row_adapters, a, b, scaling, y, base=None, workspace=
     lb = _load()
     d = _gpu(x, "x")
     M, K = x.shape
-    L, R = a.shape[0], a.shape[1]
+    L, R, _ = a.shape
     N = b.shape[1]
+    t = x.dtype
     dt = _dtype_code(x, "x", (MOE_BF16, MOE_F16))
-    for t, name in ((a, "a"), (b, "b"), (y, "y"), (base, "base")):
-        if t is not None and _codes.get(t.dtype) != dt:
-            raise ValueError(f"{name} must have the type of x")
+    xp, xl = _mat(x, "x", d, t, M, K)
+    bp, bl = (None, 0) if base is None else _mat(base, "base", d, t, M, N)
+    yp, yl = _mat(y, "y", d, t, M, N)
     ws, n, keep = _workspace(workspace, moe_decode_adapters_workspace(M, K, N, R, L), d, stream, "moe_decode_adapters")
-    _call("moe_decode_adapters", lb.moe_decode_adapters, d, stream, x.data_ptr(), _rows(x, "x", d, M, K), dt,
-          _flat(row_adapters, "row_adapters", d, M, _i32), _flat(a, "a", d, (L, R, K), a.dtype),
-          _flat(b, "b", d, (L, N, R), b.dtype), _flat(scaling, "scaling", d, L, _f32),
-          None if base is None else base.data_ptr(), 0 if base is None else _rows(base, "base", d, M, N),
-          y.data_ptr(), _rows(y, "y", d, M, N), ws, n, M, K, N, R, L)
+    for m, name in ((a, "a"), (b, "b")):
+        if m.dtype is not t and _codes.get(m.dtype) != dt:
+            raise ValueError(f"{name} must have the type of x")
+    _call("moe_decode_adapters", lb.moe_decode_adapters, d, stream, xp, xl, dt, _flat(row_adapters, "row_adapters", d, M, _i32),
+          _flat(a, "a", d, (L, R, K), a.dtype), _flat(b, "b", d, (L, N, R), b.dtype), _flat(scaling, "scaling", d, (L,), _f32),
+          bp, bl, yp, yl, ws, n, M, K, N, R, L)
     return y
 
 

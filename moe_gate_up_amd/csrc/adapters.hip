@@ -24,7 +24,14 @@ int check(int M, int K, int N, int R, int L) {
 }
 
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : R <= 128 ? 8 : 16; }
-bool few(int M) { return M <= moe::kAdFew; }
+// One launch, or three: a workgroup of the one reads all of A of its adapter, and each row of the batch is a workgroup
+// (or sixteen are).  In a graph, us, mixed adapters, one launch against three: R = 16, K = 2048 (N = 4096) 1 row 7.0, 32
+// 7.4 / 12.5, 384 16.1 / 17.4, 512 18.2 / 17.8 and with 16 rows for each adapter 30 / 17; R = 32, K = 1024 384 10.2 / 13.0; R =
+// 64, K = 4096 1 row 22.7 / 14.6, 128 32 / 15.7; R = 128, K = 4096 36 / 18.
+bool few(int M, int K, int R) {
+  const long long a = 16LL * rank_tiles(R) * K;
+  return M <= moe::kAdFew && a <= 1 << 17 && M * a <= 3 << 22;
+}
 // At most: full units, and one that is not for each adapter and for none.
 long long units_of(int M, int L, int rows) { return M / rows + (L + 1 < M ? L + 1 : M); }
 // Shares of K: enough workgroups for the chip, each of what it takes at a time at least.
@@ -38,7 +45,7 @@ int shares_of(int M, int K, int R, int L) {
 struct Layout {
   size_t order = 0, counts = 0, before = 0, v = 0, total = 0;
   Layout(int M, int K, int R, int L) {
-    if (few(M)) return;
+    if (few(M, K, R)) return;
     auto take = [&](size_t b) { const size_t r = total; total += (b + 255) & ~(size_t)255; return r; };
     order = take((size_t)M * 4);
     counts = take((size_t)(L + 1) * 4);
@@ -52,9 +59,10 @@ void go(hipStream_t st, const void* x, const void* A, const void* B, const void*
   const T *px = static_cast<const T*>(x), *pa = static_cast<const T*>(A), *pb = static_cast<const T*>(B),
           *pbase = static_cast<const T*>(base);
   T* py = static_cast<T*>(y);
-  const long long units = few(a.M) ? a.M : units_of(a.M, a.L, moe::kAdOuter);
-  const int waves = few(a.M) ? moe::ad_waves(RT) : moe::kAdOuterThreads / 64;
-  const int target = few(a.M) ? kTargetWorkgroups / 2 : 2 * kTargetWorkgroups;
+  const bool one = few(a.M, a.K, a.R);
+  const long long units = one ? a.M : units_of(a.M, a.L, moe::kAdOuter);
+  const int waves = one ? moe::ad_waves(RT) : moe::kAdOuterThreads / 64;
+  const int target = one ? kTargetWorkgroups / 2 : 2 * kTargetWorkgroups;
   // ranges of columns: enough workgroups for the chip, of work for all their wavefronts
   const int groups = (a.N + moe::kAdCols - 1) / moe::kAdCols;
   long long s = (target + units - 1) / units;
@@ -62,7 +70,7 @@ void go(hipStream_t st, const void* x, const void* A, const void* B, const void*
   s = s > most ? most : s;
   a.cols = (int)((groups + s - 1) / s) * moe::kAdCols;
   a.splits = (a.N + a.cols - 1) / a.cols;
-  if (few(a.M)) {
+  if (one) {
     hipLaunchKernelGGL((moe::adapters_few_kernel<T, RT>), dim3((unsigned)(units * a.splits)), dim3(64 * moe::ad_waves(RT)), 0, st,
                        px, pa, pb, pbase, py, a);
     return;

@@ -34,7 +34,7 @@ constexpr int kAdOuter = 32;     // and of the second
 constexpr int kAdOuterThreads = 256;
 constexpr int kAdCols = 64;      // columns of one wavefront at a time
 constexpr int kAdStep = 64;      // K of one wavefront at a time
-constexpr int kAdFew = 512;      // rows up to which the workgroups find theirs without a sort
+constexpr int kAdFew = 384;      // rows up to which the workgroups may find theirs without a sort
 constexpr int kAdMaxRank = 256;
 
 typedef float ad_f32x4 __attribute__((ext_vector_type(4)));
@@ -44,7 +44,7 @@ typedef _Float16 ad_f16x8 __attribute__((ext_vector_type(8)));
 struct AdapterArgs {
   const int32_t* ids;
   const float* scaling;
-  const int32_t* order;    // more than kAdFew rows: rows sorted by adapter, those without one last
+  const int32_t* order;    // three launches: rows sorted by adapter, those without one last
   const int32_t* counts;   // [L + 1]
   float* v;                // [shares of K, M, 16 RT], in that order of rows
   long long ld_x, ld_base, ld_y;
@@ -128,6 +128,29 @@ __global__ __launch_bounds__(64 * ad_waves(RT)) void adapters_few_kernel(const T
   const long long row = rows[min(i16, n - 1)];   // this lane's row, as an operand and as a result
   const T* Aa = A + (long long)ad * a.R * a.K;
   const T* Ba = B + (long long)ad * a.N * a.R;
+  // B and the base of the first columns are requested along with x and A
+  constexpr int S = RP / 32;
+  constexpr bool AHEAD = S <= 2;   // as far as registers go
+  Piece<T> p[2];
+  u32x4 fb[AHEAD ? S : 1][4];
+  auto request_base = [&](int n0) {
+    if (base) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) p[h].request(base + row * a.ld_base, n0 + 16 * q + 8 * h, a.N);
+    }
+  };
+  auto request_b = [&](int n0, int s) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      fb[AHEAD ? s : 0][t] =
+          ad_load(Ba + (uint32_t)min(n0 + 16 * (i16 >> 2) + 4 * t + (i16 & 3), a.N - 1) * (uint32_t)a.R, 32 * s + 8 * q, a.R);
+  };
+  int n0 = c0 + w * kAdCols;
+  if (AHEAD) {
+    request_base(n0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) request_b(n0, s);
+  }
   {
     ad_f32x4 acc[RT];
 #pragma unroll
@@ -189,7 +212,6 @@ __global__ __launch_bounds__(64 * ad_waves(RT)) void adapters_few_kernel(const T
     if (l == 0) factor[m] = __builtin_ldexpf(1.0f, -e);
   }
   __syncthreads();
-  constexpr int S = RP / 32;
   u32x4 vh[S], vl[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -197,25 +219,21 @@ __global__ __launch_bounds__(64 * ad_waves(RT)) void adapters_few_kernel(const T
     vl[s] = *reinterpret_cast<const u32x4*>(&lo[i16][32 * s + 8 * q]);
   }
   const float back = factor[i16];
-  for (int n0 = c0 + w * kAdCols; n0 < c1; n0 += NW * kAdCols) {
-    Piece<T> p[2];
-    if (base) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) p[h].request(base + row * a.ld_base, n0 + 16 * q + 8 * h, a.N);
-    }
+  for (bool begun = true; n0 < c1; n0 += NW * kAdCols, begun = false) {
+    if (!AHEAD || !begun) request_base(n0);
     ad_f32x4 acc[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      acc[t] = ad_f32x4{0, 0, 0, 0};
-      const int nr = min(n0 + 16 * (i16 >> 2) + 4 * t + (i16 & 3), a.N - 1);
+    for (int t = 0; t < 4; ++t) acc[t] = ad_f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const u32x4 f = ad_load(Ba + (long long)nr * a.R, 32 * s + 8 * q, a.R);
-        acc[t] = ad_mfma<T>(f, vh[s], acc[t]);
-        acc[t] = ad_mfma<T>(f, vl[s], acc[t]);
+    for (int s = 0; s < S; ++s) {
+      if (!AHEAD || !begun) request_b(n0, s);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        acc[t] = ad_mfma<T>(fb[AHEAD ? s : 0][t], vh[s], acc[t]);
+        acc[t] = ad_mfma<T>(fb[AHEAD ? s : 0][t], vl[s], acc[t]);
       }
     }
-    // this lane: row i16, columns n0 + 32 h + 8 q + j
+    // this lane: row i16, columns n0 + 16 q + 8 h + j
     if (i16 >= n) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

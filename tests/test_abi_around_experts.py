@@ -173,7 +173,9 @@ def test_empty_calls_do_nothing():
 
 def test_workspaces():
     assert mg.moe_decode_sort_slots_workspace(1024, 1024, 8) == 0 < mg.moe_decode_sort_slots_workspace(1025, 1024, 8)
-    assert mg.moe_decode_adapters_workspace(512, 64, 64, 8, 4) == 0 < mg.moe_decode_adapters_workspace(513, 64, 64, 8, 4)
+    assert mg.moe_decode_adapters_workspace(384, 64, 64, 8, 4) == 0 < mg.moe_decode_adapters_workspace(385, 64, 64, 8, 4)
+    assert mg.moe_decode_adapters_workspace(96, 8192, 64, 16, 4) == 0 < mg.moe_decode_adapters_workspace(97, 8192, 64, 16, 4)
+    assert mg.moe_decode_adapters_workspace(1, 2048, 64, 64, 4) == 0 < mg.moe_decode_adapters_workspace(1, 2056, 64, 64, 4)
     assert mg.moe_decode_rms_norm_backward_workspace(1, 100) >= 400
     for fn, args in ((mg.moe_decode_sort_slots_workspace, (1 << 24, 8, 1)), (mg.moe_decode_adapters_workspace, (1, 4, 1, 8, 1)),
                      (mg.moe_decode_rms_norm_backward_workspace, (1, 0))):
