@@ -241,8 +241,7 @@ __global__ __launch_bounds__(64 * ad_waves(RT)) void adapters_few_kernel(const T
       if (c >= c1) continue;
       float f[kPiece];
       if (base) {
-        if (base == y) p[h].settle_own(base + row * a.ld_base, c, a.N);
-        else p[h].settle(c, a.N);
+        p[h].settle(c, a.N, base == y ? base + row * a.ld_base : nullptr);
         p[h].values(f);
       }
 #pragma unroll
@@ -508,8 +507,7 @@ __global__ __launch_bounds__(kAdOuterThreads) void adapters_outer_kernel(const T
         const float back = factor[m];
         float g[kPiece];
         if (base) {
-          if (base == y) p[i].settle_own(base + row[i] * a.ld_base, n0 + col, a.N);
-          else p[i].settle(n0 + col, a.N);
+          p[i].settle(n0 + col, a.N, base == y ? base + row[i] * a.ld_base : nullptr);
           p[i].values(g);
         }
 #pragma unroll

@@ -68,8 +68,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const T* __res
   }
   if (add) {
     float f[kPiece];
-    if (add == y) base.settle_own(add + (long long)t * a.ld_add, c, a.N);
-    else base.settle(c, a.N);
+    base.settle(c, a.N, add == y ? add + (long long)t * a.ld_add : nullptr);
     base.values(f);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) sum[i] += f[i];

@@ -30,7 +30,8 @@ struct Piece {
 
   // Elements c .. c + 7 of a row of n; those behind the row are 0 and not read.  In two steps: request() makes the same
   // loads for every lane (one under a condition of the lane's would be waited for at its end), of the row's last 8 where
-  // fewer are left, and settle() moves those into place.
+  // fewer are left, and settle() moves those into place.  A row that is written in place is given to it as `own`: another
+  // lane may have stored the elements in front of a short piece since its request, so the lane's own are read once more.
   __device__ __forceinline__ void request(const T* row, int c, int n) {
     if (n >= kPiece) {
       const any4* from = reinterpret_cast<const any4*>(row + (uint32_t)min(c, n - kPiece));
@@ -47,8 +48,15 @@ struct Piece {
       __builtin_memcpy(v, t, sizeof(v));
     }
   }
-  __device__ __forceinline__ void settle(int c, int n) {
+  __device__ __forceinline__ void settle(int c, int n, const T* own = nullptr) {
     if (c + kPiece <= n || n < kPiece) return;
+    if (own) {
+      T t[kPiece];
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) t[i] = c + i < n ? own[c + i] : (T)0.0f;
+      __builtin_memcpy(v, t, sizeof(v));
+      return;
+    }
     const int s = min(c + kPiece - n, kPiece);   // elements that are not the lane's come first
     constexpr int K = 4 * kWords;
 #pragma unroll
@@ -62,15 +70,6 @@ struct Piece {
         v[i] = (s & step) ? moved : v[i];
       }
     }
-  }
-  // settle() for a row that is written in place: another lane may have stored the elements in front of a short piece
-  // between its request and here, so the lane's own are read once more.
-  __device__ __forceinline__ void settle_own(const T* row, int c, int n) {
-    if (c + kPiece <= n || n < kPiece) return;
-    T t[kPiece];
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) t[i] = c + i < n ? row[c + i] : (T)0.0f;
-    __builtin_memcpy(v, t, sizeof(v));
   }
   __device__ __forceinline__ void store(T* row, int c, int n) const { put<false>(row, c, n); }
   // As store(), past the caches: for results much larger than they are, which would push out what is still to be read.

@@ -106,8 +106,7 @@ __global__ __launch_bounds__(norm_threads(WR)) void rms_norm_kernel(const T* __r
   for (int i = 0; i < P; ++i) {
     r[i].settle(column(i), a.H);
     if (res) {
-      if (res == sum) t[i].settle_own(res + m * a.ld_res, column(i), a.H);
-      else t[i].settle(column(i), a.H);
+      t[i].settle(column(i), a.H, res == sum ? res + m * a.ld_res : nullptr);
       float f[kPiece], g[kPiece];
       r[i].values(f);
       t[i].values(g);

@@ -77,8 +77,7 @@ __global__ __launch_bounds__(kNormBackThreads) void rms_norm_backward_kernel(con
       pr[i].values(n[i]);
       pg[i].values(g[i]);
       if (dsum) {
-        if (dsum == dx) ps[i].settle_own(dsum + (on ? m : a.M - 1) * a.ld_dsum, column(i), a.H);
-        else ps[i].settle(column(i), a.H);
+        ps[i].settle(column(i), a.H, dsum == dx ? dsum + (on ? m : a.M - 1) * a.ld_dsum : nullptr);
         ps[i].values(t[i]);
       } else {
 #pragma unroll
