@@ -6,6 +6,10 @@
 // over its rows.  The next row's inputs are requested before the present one is worked
 // on.  The wavefronts' sums for dweight are halved pairwise in LDS, the workgroups' are
 // added by a second launch.
+//
+// Memory bounds it: 16384 x 2048 bf16 with dsum 50 us for 268 MB (5.4 TB/s; a copy
+// 6.3), and 5 for the second launch.  One piece a lane and one workgroup a CU: four pieces,
+// so that a wavefront holds a row, spill (159 us, and 92 at 8 wavefronts a CU).
 #pragma once
 
 #include "rms_norm.hpp"

@@ -5,14 +5,23 @@
 // A row of up to 256 experts lies in 16 lanes (else in a whole wavefront): each
 // group of experts in its own LG lanes, LG the largest power of two that the
 // groups leave, so that a group's score is log2 LG DPP steps and a row's maximum
-// 4 (or 6).  The groups are taken one by one, then the experts: the maximum of the
-// order-preserving keys in play, the lowest expert that holds it, and that key out
-// of play.  Selection j lands in the row's lane j, which works out its weight.
+// 4 (or 6).  Each lane sorts its keys once; then every selection is the maximum of
+// the lanes' first keys, and the lane that had it moves its others up.  Groups are taken
+// alike before that.  Selection j lands in the row's lane j, which works out its weight.
 //
 // Choices are those of 64 bits.  Without a bias they go by the logits themselves.
-// With one (or by sums of two scores) the FP32 values' errors are known, and a row
-// in which two of them that the choice hangs on lie nearer than that is done again
-// in FP64 by the whole wavefront (one row in some hundreds).
+// With one (or by sums of two scores) the FP32 values' errors are known; neighbours in the
+// order of choice that lie nearer than those are compared in FP64, one exponential a
+// lane, and a row that this does not settle (or whose groups are as near) is done again
+// in FP64 by the whole wavefront at its end: about one row in 10000 of those measured.
+//
+// Vector instructions bound it: 262144 tokens of 128 experts, FP32, sigmoid, bias, 8 groups, the two
+// largest, top-8: 72 us for 151 MB (2.1 TB/s), 424 vector instructions for 4 rows, of them
+// 96 quarters of an exponential or reciprocal, 120 for the 8 selections and 38 for the sort;
+// without the rows done again 64.  Keys and numbers in two registers and a search for
+// the lowest number each time took 188.  4 workgroups a CU that go on to the next rows,
+// whose logits are requested ahead; one workgroup for 16 rows 93.  32 tokens of 256 experts: 5.4 us.
+// The gradient: 41 us for 285 MB (6.9 TB/s, some of the logits from the memory-side cache).
 #pragma once
 
 #include "balance.hpp"

@@ -10,6 +10,7 @@
 // of each expert, and the parts of the second add up what lies before them.  Counts
 // are added in LDS by one lane for all of its round that share its expert: lanes of one
 // address are served one after another (32768 slots counted lane by lane 20 us).
+// Latencies bound it: 32768 slots of 128 experts 3.6 + 5.2 us, 8192 of 9 in one launch 7.2.
 #pragma once
 
 #include "prims.hpp"
