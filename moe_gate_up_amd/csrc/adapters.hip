@@ -45,7 +45,7 @@ int shares_of(int M, int K, int R, int L) {
 struct Layout {
   size_t order = 0, counts = 0, before = 0, v = 0, total = 0;
   Layout(int M, int K, int R, int L) {
-    if (few(M, K, R)) return;
+    if (M == 0 || few(M, K, R)) return;   // no rows have no units, whose number divides in shares_of()
     auto take = [&](size_t b) { const size_t r = total; total += (b + 255) & ~(size_t)255; return r; };
     order = take((size_t)M * 4);
     counts = take((size_t)(L + 1) * 4);

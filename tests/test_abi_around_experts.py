@@ -198,3 +198,9 @@ def test_binding_refuses_cpu_tensors():
                  lambda: mg.moe_decode_adapters(f(4, 16, **h), f(4, **i32), f(2, 8, 16, **h), f(2, 8, 8, **h), f(2), f(4, 8, **h))):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("K,R", [(8, 8), (4096, 64), (4096, 256), (1 << 20, 256)])
+def test_adapters_of_no_rows(K, R):
+    assert mg.moe_decode_adapters_workspace(0, K, 4096, R, 64) == 0
+    assert adapters(M=0, K=K, R=R, ws=None, ws_bytes=0) == mg.MOE_OK
