@@ -8,12 +8,12 @@
 // repeats v.
 // Many rows: they are sorted by adapter first, and units of rows of one adapter go
 // through two launches, each of which streams: one forms v of 128 rows for a share of K, A's
-// share in LDS and a wavefront's 16 rows of x requested all at once; the other adds the
+// share in LDS and a wavefront's 16 rows of x requested all at once behind it; the other adds the
 // shares of 32 rows and goes on as above.
 //
 // 32 rows with adapters of their own, 2048 -> 4096, rank 16: 7.7 us, four memory latencies
 // one behind the other.  8192 rows of 8 adapters, 4096 -> 4096, rank 64: 7.2 us for the
-// sort, 25 and 38 for the products of 67 and 134 MB (2.7 and 3.5 TB/s): each unit waits for
+// sort, 22 and 38 for the products of 67 and 134 MB (3.0 and 3.5 TB/s): each unit waits for
 // its rows' numbers, then for its operands, and a CU holds one workgroup of the first
 // product and two of the second.  Both products in one launch, 16 rows a workgroup, took
 // 126: neither x nor the base was requested far enough ahead.
@@ -315,23 +315,9 @@ __global__ __launch_bounds__(kAdInner * 4) void adapters_inner_kernel(const T* _
   for (int t = 0; t < RT; ++t) acc[t] = ad_f32x4{0, 0, 0, 0};
   const int k1 = min((share + 1) * a.span, a.K);
   for (int k0 = share * a.span; k0 < k1; k0 += SPAN) {
-    u32x4 fx[STEPS][2];
-    if (on) {
-#pragma unroll
-      for (int u = 0; u < STEPS; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          fx[u][h] = *reinterpret_cast<const u32x4*>(xr + (uint32_t)min(k0 + u * kAdStep + 16 * q + 8 * h, a.K - 8));
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int EACH = 16 * RT * PIECES / NT, U = EACH < 4 ? EACH : 4;   // pieces of A of a thread, requested 4 at a time
-    for (int i0 = 0; i0 < EACH; i0 += U) {
-      u32x4 f[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int n = (i0 + i) * NT + tid, r = n / PIECES, k = k0 + 8 * (n % PIECES);
-        f[i] = *reinterpret_cast<const u32x4*>(Aa + (uint32_t)min(r, a.R - 1) * (uint32_t)a.K + (uint32_t)min(k, a.K - 8));
-      }
+    constexpr int EACH = 16 * RT * PIECES / NT, U = 4;   // pieces of A of a thread, requested U at a time
+    u32x4 f[U], fx[STEPS][2];
+    auto place = [&](int i0) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int n = (i0 + i) * NT + tid, r = n / PIECES, p = n % PIECES;
@@ -339,7 +325,34 @@ __global__ __launch_bounds__(kAdInner * 4) void adapters_inner_kernel(const T* _
         for (int j = 0; j < 4; ++j) f[i].v[j] = k0 + 8 * p < k1 ? f[i].v[j] : 0u;
         lds[r * PIECES + (p ^ (r & 15))] = f[i];
       }
+    };
+    // A before x: loads are waited for in order, and A's, from L2, would be behind all of x (24.6 us, and 21.7 so)
+    for (int i0 = 0; i0 < EACH; i0 += U) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int n = (i0 + i) * NT + tid, r = n / PIECES, k = k0 + 8 * (n % PIECES);
+        f[i] = *reinterpret_cast<const u32x4*>(Aa + (uint32_t)min(r, a.R - 1) * (uint32_t)a.K + (uint32_t)min(k, a.K - 8));
+      }
+      if (i0 + U < EACH) place(i0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (on) {
+      if (k0 + SPAN <= a.K) {   // offsets that the instructions hold: a register each spills
+        const T* from = xr + (uint32_t)(k0 + 16 * q);
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) fx[u][h] = *reinterpret_cast<const u32x4*>(from + u * kAdStep + 8 * h);
+      } else {
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            fx[u][h] = *reinterpret_cast<const u32x4*>(xr + (uint32_t)min(k0 + u * kAdStep + 16 * q + 8 * h, a.K - 8));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    place(EACH - U);
     __syncthreads();
     if (on) {
 #pragma unroll
