@@ -239,7 +239,8 @@ __device__ __forceinline__ float sigmoid_exact(float l) {
 
 // Keys.  What decides (c: logit, or score + bias) becomes a whole number q of the row's range, of 32 - BITS bits,
 // and 1024 (256) less the expert's number the bits below: one unsigned maximum finds the largest and of equals the
-// lowest expert, and no two keys are alike.  0 is an expert out of play, q = 0 one that is ruled out.
+// lowest expert, and no two keys are alike.  0 is an expert out of play, q = 0 one that is ruled out; every other
+// has q >= 1, since c is taken from the range's lower end first: -lo * unit + 1 would be rounded, to less than 1 as well.
 template <typename T, int LR, int V, int C, int BY>
 __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* __restrict__ logits, ScoreArgs a) {
   constexpr int RW = 64 / LR;
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
   const bool slot = l < a.k;
 
   // What the lane's experts have for every row: the low bits of their keys (0: no such expert), and what -inf and no
-  // expert are made NaN with: c = x * rule + x of logits, score + (x * 0 + rule) where rule is the bias.
+  // expert are made NaN with: c = x * rule + x of logits, score + (x * 0 + rule) where rule is the bias less the smallest.
   uint32_t code[V];
   float rule[V], bias_hi = 0.0f, bias_lo = 0.0f;
 #pragma unroll
@@ -269,8 +270,12 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
     bias_hi = v ? fmaxf(bias_hi, rule[v]) : rule[v];
     bias_lo = v ? fminf(bias_lo, rule[v]) : rule[v];
   }
-  // scores lie in [0, 1]: with the bias, one range for all rows
-  const float score_hi = 1.0f + row_top<LR>(bias_hi), score_lo = row_low<LR>(bias_lo);
+  // scores lie in [0, 1]: with the bias, one range for all rows, whose lower end is 0
+  const float least = row_low<LR>(bias_lo), score_hi = 1.0f + (row_top<LR>(bias_hi) - least);
+  if constexpr (!by_logit) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) rule[v] -= least;
+  }
 
   auto weigh = [&](float logit, float m, float sum) {
     float w;
@@ -347,9 +352,9 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
       sum = row_sum<LR>(sum);
       inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
-    auto score = [&](float f) {
+    auto score = [&](float f) {   // of a logit less m (a sigmoid's is 0)
       return sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(f * -1.44269504f))
-                     : __builtin_amdgcn_exp2f((f - m) * 1.44269504f) * inv;
+                     : __builtin_amdgcn_exp2f(f * 1.44269504f) * inv;
     };
     // A score in FP64, and whether one's choice lies above another's.  A softmax's sum is that of FP32, whose error both
     // have in common: 2^-18 of the scores' difference.
@@ -363,11 +368,11 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
     };
     // Errors of FP32 scores.  Sigmoid: e^-l within (1.5 |l| + 2) 2^-24, and |l| s (1 - s) < 0.23, the reciprocal and the
     // sum of 1: 5 2^-24 in all.  Softmax: (|l - m| + 3) 2^-23 and the sum's 10 2^-23 of s, |l - m| s < 0.4 of the largest
-    // score `inv`: 2^-19 inv.  A bias's sum rounds by 2^-24 |c|.  Logits have none.
+    // score `inv`: 2^-19 inv.  Logits have none.
     const float err = by_logit ? 0.0f : sigmoid ? 5.0f * 0x1p-24f : 0x1p-19f * inv;
 
-    // what decides; NaN: ruled out or no expert, which maxima and minima pass over
-    float c[V], hi = score_hi, lo = score_lo, hi_lane = 0.0f;
+    // what decides, from the range's lower end; NaN: ruled out or no expert, which maxima and minima pass over
+    float c[V], hi = score_hi, lo = 0.0f, hi_lane = 0.0f;
     if (by_logit) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -378,22 +383,24 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
       hi_lane = hi;
       hi = row_top<LR>(hi);
       lo = row_low<LR>(lo);
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] -= lo;
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = score(x[v]) + __builtin_fmaf(x[v], 0.0f, rule[v]);
+      for (int v = 0; v < V; ++v) c[v] = score(x[v] - m) + __builtin_fmaf(x[v], 0.0f, rule[v]);
     }
-    // q = 1 + (c - lo) * unit in one rounding, truncated and cut off at both ends: it never goes down where c goes up
+    // q = 1 + c * unit, truncated and cut off above: each step never goes down where the logit or score + bias goes up
     const float range = hi - lo;
     const float unit = range > 0x1p-100f && range < kInf ? (kTop - 4.0f) / range : 1.0f;
-    const float start = __builtin_fmaf(-lo, unit, 1.0f);
-    // two experts further apart than this are in order: both errors, the product's rounding, the truncation
+    // Two experts further apart than this are in order: both scores' errors; the biases' difference, up to range - 1, and
+    // its sum with the score, up to range, round by 2^-24 of themselves for each; the product's rounding, the truncation.
     const uint32_t near =
-        by_logit ? 4u : (uint32_t)fminf((2.0f * err + 0x1p-23f * (__builtin_fabsf(hi) + __builtin_fabsf(lo))) * unit + 3.0f, kTop);
+        by_logit ? 4u : (uint32_t)fminf((2.0f * err + 0x1p-23f * (2.0f * range - 1.0f)) * unit + 3.0f, kTop);
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       // the middle one of three; of a NaN and two numbers the smaller
-      const float q = __builtin_amdgcn_fmed3f(__builtin_fmaf(c[v], unit, start), 0.0f, kTop);
+      const float q = __builtin_amdgcn_fmed3f(__builtin_fmaf(c[v], unit, 1.0f), 0.0f, kTop);
       key[v] = (uint32_t)q << BITS | code[v];
     }
     bool doubt = !(range < kInf) && range == range;   // not a number: all are ruled out
@@ -435,9 +442,9 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
           doubt |= g < a.G && q1 != 0u && q2 == 0u;   // one alone is left: not a sum of two
           s = (q1 + q2) >> 1;
           within = near + 2u;
-          if (by_logit) {   // of the scores, whose order the logits' is
-            const float back = 1.0f / unit, l1 = lo + (float)(q1 - 1u) * back, l2 = lo + (float)(q2 - 1u) * back;
-            const float e = (sigmoid ? 0x1p-21f : 0x1p-19f * inv) + 8.0f * back * (sigmoid ? 0.25f : inv) + 0x1p-22f;
+          if (by_logit) {   // of the scores, whose order the logits' is; a logit less m is known to 5 units
+            const float back = 1.0f / unit, l1 = lo - m + (float)(q1 - 1u) * back, l2 = lo - m + (float)(q2 - 1u) * back;
+            const float e = (sigmoid ? 0x1p-21f : 0x1p-19f * inv) + 10.0f * back * (sigmoid ? 0.25f : inv) + 0x1p-22f;
             s = q1 ? 1u + (uint32_t)fminf((score(l1) + score(l2)) * (0.5f * (kTop - 4.0f)), kTop) : 0u;
             within = (uint32_t)fminf(2.0f * e * kTop + 4.0f, kTop);
           }
