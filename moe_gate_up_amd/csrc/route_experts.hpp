@@ -403,7 +403,8 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
       const float q = __builtin_amdgcn_fmed3f(__builtin_fmaf(c[v], unit, 1.0f), 0.0f, kTop);
       key[v] = (uint32_t)q << BITS | code[v];
     }
-    bool doubt = !(range < kInf) && range == range;   // not a number: all are ruled out
+    // biases whose range is not a finite number go to 64 bits; of logits, not a number: all are ruled out
+    bool doubt = !(range < kInf) && (!by_logit || range == range);
     sort_keys<V>(key);
     if (grouped) {
       uint32_t gk, last = 0;

@@ -59,3 +59,18 @@ def test_logits_far_from_zero(dev, offset):  # noqa: F811
         for top2 in (False, True):
             print(f"offset {offset} E={E} groups={groups} top2={top2}", flush=True)
             check(l, None, k, False, True, groups, top, top2)
+
+
+def test_infinite_biases(dev):  # noqa: F811
+    """-inf puts an expert behind all others, as it does in 64 bits, +inf in front; a row may also be ruled out by its logits."""
+    for E, k, groups, top in ((64, 6, 1, 1), (128, 8, 8, 4), (512, 8, 1, 1)):
+        base = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+        l = make(E, 60, E, torch.float32, dev)
+        l[::2] = few_in_play(E, 30, E, k + 1, torch.float32, dev)
+        for value in (-INF, INF):
+            for on in (slice(5, 6), slice(0, E - 3), slice(0, E)):
+                bias = base.clone()
+                bias[on] = value
+                for sigmoid in (False, True):
+                    print(f"bias {value} of {on} E={E} sigmoid={sigmoid}", flush=True)
+                    check(l, bias.to(dev), k, sigmoid, True, groups, top, groups > 1)
