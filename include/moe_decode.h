@@ -433,13 +433,13 @@ int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int *variant, int *wo
  *   - of their experts token t takes the k with the largest c, largest first, the
  *     lower id first among equals: topk_ids[t, j].
  *   - topk_weights[t, j] = scale * s of that expert (without the bias), with
- *     MOE_ROUTE_RENORM over the sum of the k (0 where that sum is 0).
+ *     MOE_ROUTE_RENORM over the sum of the k (0 where that sum is 0 in 64 bits).
  * Choices are those of c in 64 bits; without a bias, experts (and groups by their
- * largest) go by the logits.  Weights are FP32.  A logit of -inf rules an expert
- * out: it comes behind all others of the groups that stay, its score is 0, a group
- * of such comes last.  Ids are always different from each other and in [0, E);
- * with a logit of +inf or NaN in the row they and the weights are not specified
- * otherwise.
+ * largest) go by the logits.  Weights are FP32; a score below 2^-126 may count as 0.
+ * A logit of -inf rules an expert out: it comes behind all others of the groups that
+ * stay, its score is 0, a group of such comes last.  Ids are always different from
+ * each other and in [0, E); with a logit of +inf or NaN in the row they and the
+ * weights are not specified otherwise.
  *   logits        [T, E] of `dtype` (MOE_F32 or MOE_BF16), row t at t * ld elements
  *   bias          fp32 [E] or NULL (0)
  *   topk_ids      int32 [T, k];  topk_weights  fp32 [T, k]

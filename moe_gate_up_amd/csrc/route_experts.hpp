@@ -231,6 +231,11 @@ __device__ __forceinline__ float exp_below(float x) {
   return x < -100.0f ? 0.0f : v;   // also -inf, whose rest is NaN
 }
 
+// Renormalised sigmoid scores whose sum is less than this (all logits below -44) are quotients of e^(l - M) instead, M
+// the largest of their logits: FP32 has no e^l below -87, but the quotients.  Down to M = -745, where 64 bits have
+// no e^l either and the sum is 0.  Such rows are done again.
+constexpr float kScoreSumSmall = 0x1p-64f, kScoreLogitNone = -745.13f;
+
 // 1 / (1 + e^-l): a = e^-|l| cannot overflow.
 __device__ __forceinline__ float sigmoid_exact(float l) {
   const float a = exp_below(-__builtin_fabsf(l));
@@ -277,7 +282,8 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
     for (int v = 0; v < V; ++v) rule[v] -= least;
   }
 
-  auto weigh = [&](float logit, float m, float sum) {
+  // `sum`: of a softmax's exponentials; with renorm it becomes the selections'.
+  auto weigh = [&](float logit, float m, float& sum, bool again) {
     float w;
     if (sigmoid) {
       w = sigmoid_exact(logit);
@@ -287,7 +293,14 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
       w = exp_below(logit - m);
     }
     w = slot ? w : 0.0f;
-    if (renorm) sum = row_sum<LR>(w);
+    if (renorm) {
+      sum = row_sum<LR>(w);
+      if (again && sigmoid && sum < kScoreSumSmall) {   // of the wavefront's one row
+        m = row_top<LR>(slot ? logit : -kInf);
+        w = slot && m > kScoreLogitNone ? exp_below(logit - m) : 0.0f;
+        sum = row_sum<LR>(w);
+      }
+    }
     if (renorm || !sigmoid) w = sum == 0.0f ? 0.0f : w / sum;
     return w * a.scale;
   };
@@ -503,9 +516,10 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
         close = close && !doubt && M >> BITS && qk - (M >> BITS) <= near;
       }
     }
+    const float w = weigh(logit, m, sum, false);
+    doubt |= sigmoid && renorm && slot && sum < kScoreSumSmall && logit > kScoreLogitNone;
     doubt = row_max_u32<LR>(doubt ? 1u : 0u) != 0u;
     if (__builtin_amdgcn_ballot_w64(doubt)) again |= 1ull << (round & 63);
-    const float w = weigh(logit, m, sum);
     if (slot && first + lane / LR < a.T) {
       a.ids[(long long)t * a.k + l] = doubt && l == 0 ? -1 : id;
       a.weights[(long long)t * a.k + l] = w;
@@ -532,7 +546,7 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_kernel(const T* _
         for (int e = l; e < a.E; e += LR) sum += exp_below(elem_f32(row[e]) - m);
         sum = row_sum<LR>(sum);
       }
-      const float w = weigh(slot ? elem_f32(row[id]) : 0.0f, m, sum);
+      const float w = weigh(slot ? elem_f32(row[id]) : 0.0f, m, sum, true);
       if (slot && lane < LR) {
         ids[l] = id;
         a.weights[(long long)t * a.k + l] = w;
@@ -592,7 +606,13 @@ __global__ __launch_bounds__(kScoreThreads) void route_experts_backward_kernel(
       s = slot ? expf(logit - m) : 0.0f;
     }
     if (renorm) {
-      const float sum = row_sum<LR>(s);
+      float sum = row_sum<LR>(s);
+      const bool small = sigmoid && sum < kScoreSumSmall;
+      if (__builtin_amdgcn_ballot_w64(small)) {
+        m = row_max<LR>(logit);
+        s = !small ? s : m > kScoreLogitNone ? expf(logit - m) : 0.0f;
+        sum = row_sum<LR>(s);
+      }
       s = sum == 0.0f ? 0.0f : s / sum;
       dot = row_sum<LR>(slot ? g * s : 0.0f);
     }
