@@ -552,7 +552,7 @@ int moe_decode_rms_norm_backward(const void *dy, long long ld_dy, const void *r,
  * `workspace` is device memory of at least moe_decode_adapters_workspace() bytes,
  * 256-byte aligned, used until the launches complete (calls that may overlap in time
  * need one each); it need not be cleared, and where that says 0 bytes it is not
- * looked at.  M == 0 is a valid no-op. */
+ * looked at.  The size never goes down where M grows.  M == 0 is a valid no-op. */
 int moe_decode_adapters_workspace(int M, int K, int N, int R, int L, size_t *bytes);
 int moe_decode_adapters(const void *x, long long ld_x, int dtype, const int32_t *row_adapters,
                         const void *a, const void *b, const float *scaling,

@@ -40,17 +40,26 @@ int shares_of(int M, int K, int R, int L) {
   const int most = (K + moe::ad_span(rank_tiles(R)) - 1) / moe::ad_span(rank_tiles(R));
   return (int)(want < most ? want : most);
 }
+// Rows of v that no call of up to M rows passes, so that one workspace does for all smaller batches: M times the shares is
+// M (1 + floor(255 / units)) at most, where units are M or more up to L + 1 rows, and more than M / 128 + L beyond.
+size_t inner_rows(int M, int K, int R, int L) {
+  constexpr long long want = kTargetWorkgroups / 2 - 1;
+  const long long most = (K + moe::ad_span(rank_tiles(R)) - 1) / moe::ad_span(rank_tiles(R));
+  const long long of_units = want * moe::kAdInner * M / (M + (long long)moe::kAdInner * L);
+  const long long rows = M + (of_units > want ? of_units : want);
+  return (size_t)(rows < most * M ? rows : most * M);
+}
 
 // Workspace of many rows: their order by adapter, the adapters' numbers of rows, the sort's parts' and v.
 struct Layout {
   size_t order = 0, counts = 0, before = 0, v = 0, total = 0;
   Layout(int M, int K, int R, int L) {
-    if (M == 0 || few(M, K, R)) return;   // no rows have no units, whose number divides in shares_of()
+    if (M == 0 || few(M, K, R)) return;
     auto take = [&](size_t b) { const size_t r = total; total += (b + 255) & ~(size_t)255; return r; };
     order = take((size_t)M * 4);
     counts = take((size_t)(L + 1) * 4);
     before = take(moe::sort_counts(M, L + 1) * 4);
-    v = take((size_t)shares_of(M, K, R, L) * M * rank_tiles(R) * 64);
+    v = take(inner_rows(M, K, R, L) * rank_tiles(R) * 64);
   }
 };
 
