@@ -646,7 +646,7 @@ def moe_decode_rms_norm(x, weight, eps, y=None, q=None, scales=None, residual=No
                         stream=None):
     """The root-mean-square norm of x [M,H] (+ residual) times weight [H] (x's type or fp32): y [M,H], and / or q [M,H]
     E4M3 codes (uint8) with scales fp32 [M, ceil(H/128)]; sum_out [M,H]: x + residual (it may be the residual); rstd
-    fp32 [M] (see include/moe_decode.h)."""
+    fp32 [M] (see include/moe_decode.h).  Returns (y, q, scales, sum_out, rstd), None where none was given."""
     L = _load()
     d = _gpu(x, "x")
     M, H = x.shape
@@ -661,6 +661,7 @@ def moe_decode_rms_norm(x, weight, eps, y=None, q=None, scales=None, residual=No
           eps, yp, yl, None if q is None else _flat(q, "q", d, (M, H), _u8),
           None if scales is None else _flat(scales, "scales", d, (M, -(-H // 128)), _f32), sp, sl,
           None if rstd is None else _flat(rstd, "rstd", d, (M,), _f32), M, H, MOE_QUANT_POW2 if pow2 else 0)
+    return y, q, scales, sum_out, rstd
 
 
 @functools.lru_cache(maxsize=256)
