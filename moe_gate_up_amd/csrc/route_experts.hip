@@ -52,16 +52,18 @@ struct Choose {
     else hipLaunchKernelGGL((moe::route_experts_kernel<T, LR, V, C, moe::kBySoftmax>), grid, block, 0, st, x, a);
   }
 };
-template <typename T, int LR, int C, typename F>
+// More than 16 of a lane: in groups, which leave lanes without an expert.
+template <typename T, int LR, int C, int MOST, typename F>
 void by_experts_of_lane(int n, const F& f) {
+  static_assert(MOST == 16 || MOST == 32, "experts of a lane");
   if (n <= 4) f.template operator()<T, LR, 4, C>();
   else if (n <= 8) f.template operator()<T, LR, 8, C>();
   else if (n <= 16) f.template operator()<T, LR, 16, C>();
-  else f.template operator()<T, LR, 32, C>();
+  else if constexpr (MOST > 16) f.template operator()<T, LR, 32, C>();
 }
 template <typename T, int LR, typename F>
 void by_piece(bool whole, int n, const F& f) {
-  whole ? by_experts_of_lane<T, LR, 4>(n, f) : by_experts_of_lane<T, LR, 1>(n, f);
+  whole ? by_experts_of_lane<T, LR, 4, 32>(n, f) : by_experts_of_lane<T, LR, 1, 32>(n, f);
 }
 
 struct RouteBackward {
@@ -85,8 +87,8 @@ struct RouteBackward {
 // 16 lanes a row up to 256 experts and 16 slots, else a whole wavefront.
 template <typename T, int C>
 void backward_by_size(int E, int k, const RouteBackward& f) {
-  if (k > 16 || E > 256) by_experts_of_lane<T, 64, C>((E + 63) / 64, f);
-  else by_experts_of_lane<T, 16, C>((E + 15) / 16, f);
+  if (k > 16 || E > 256) by_experts_of_lane<T, 64, C, 16>((E + 63) / 64, f);
+  else by_experts_of_lane<T, 16, C, 16>((E + 15) / 16, f);
 }
 
 // ---------------------------------------------------------------- slots by expert
