@@ -470,7 +470,7 @@ int moe_decode_route_experts_backward(const void *logits, long long ld, int dtyp
  * device memory of at least moe_decode_sort_slots_workspace() bytes, 256-byte
  * aligned, used until the launches complete (calls that may overlap in time need one
  * each); it need not be cleared, and where that says 0 bytes it is not looked at.
- * With T == 0 counts, where they are given, are set to 0; nothing else is looked at. */
+ * T == 0 is a valid no-op that writes nothing. */
 int moe_decode_sort_slots_workspace(int T, int E, int k, size_t *bytes);
 int moe_decode_sort_slots(const int32_t *topk_ids, const uint8_t *valid, int32_t *counts, int32_t *x_rows,
                           int32_t *positions, void *workspace, size_t workspace_bytes,
@@ -525,8 +525,7 @@ int moe_decode_combine_backward(const void *dy, long long ld_dy, const void *row
  * until the launches complete (calls that may overlap in time need one each); it need
  * not be cleared.
  * Limits: H <= 32768; M < 2^26 up to 1024 columns, 2^24 up to 16384, else 2^22;
- * strides up to 2^30.  M == 0 is a valid no-op that writes nothing: dweight, whose sums
- * are then of no rows, keeps what it holds. */
+ * strides up to 2^30.  M == 0 is a valid no-op that writes nothing. */
 int moe_decode_rms_norm(const void *x, long long ld_x, const void *residual, long long ld_residual, int dtype,
                         const void *weight, int weight_dtype, float eps, void *y, long long ld_y,
                         uint8_t *q, float *scales, void *sum, long long ld_sum, float *rstd,

@@ -201,13 +201,7 @@ int moe_decode_sort_slots(const int32_t* topk_ids, const uint8_t* valid, int32_t
                           int32_t* positions, void* workspace, size_t workspace_bytes, int T, int E, int k, void* stream) {
   const int rc = check_sort(T, E, k);
   if (rc) return rc;
-  if (T == 0) {
-    if (!aligned(counts, 4)) return MOE_ERR_ALIGN;
-    if (!counts) return MOE_OK;
-    (void)hipGetLastError();
-    moe::launch_sort_none(static_cast<hipStream_t>(stream), counts, E);
-    return launched();
-  }
+  if (T == 0) return MOE_OK;
   const int slots = T * k;
   const size_t need = moe::sort_counts(slots, E) * 4, slot_bytes = (size_t)slots * 4;
   if (!need) workspace = nullptr;

@@ -222,12 +222,4 @@ inline void launch_sort(hipStream_t st, const SortArgs& a) {
   else hipLaunchKernelGGL((sort_place_kernel<false, false>), grid, block, 0, st, a);
 }
 
-// No slots: every expert has 0.
-static __global__ __launch_bounds__(kSortThreads) void sort_none_kernel(int32_t* __restrict__ counts, int E) {
-  if ((int)threadIdx.x < E) counts[threadIdx.x] = 0;
-}
-inline void launch_sort_none(hipStream_t st, int32_t* counts, int E) {
-  hipLaunchKernelGGL(sort_none_kernel, dim3(1), dim3(kSortThreads), 0, st, counts, E);
-}
-
 }  // namespace moe
