@@ -428,12 +428,14 @@ int moe_decode_matmul_fp8_plan(int M, int N, int K, int E, int *variant, int *wo
  * 1 / (1 + e^-l_te) with MOE_ROUTE_SIGMOID, and c_te = s_te + bias_e:
  *   - the experts lie in `groups` groups of E / groups neighbours.  A group's score
  *     is its largest c, or with MOE_ROUTE_GROUP_TOP2 the sum of its two largest (the
- *     one, where one expert alone is not ruled out).  The top_groups groups with the
- *     largest scores stay, the lower group first among equals.
+ *     one, where one expert alone is not ruled out; of groups of one expert the flag
+ *     says nothing).  The top_groups groups with the largest scores stay, the lower
+ *     group first among equals.
  *   - of their experts token t takes the k with the largest c, largest first, the
  *     lower id first among equals: topk_ids[t, j].
  *   - topk_weights[t, j] = scale * s of that expert (without the bias), with
- *     MOE_ROUTE_RENORM over the sum of the k (0 where that sum is 0 in 64 bits).
+ *     MOE_ROUTE_RENORM over the sum of the k (0 where all k are ruled out, or of
+ *     sigmoid scores that are 0 in 64 bits too).
  * Choices are those of c in 64 bits; without a bias, experts (and groups by their
  * largest) go by the logits.  Weights are FP32; a score below 2^-126 may count as 0.
  * A logit of -inf rules an expert out: it comes behind all others of the groups that
@@ -470,7 +472,8 @@ int moe_decode_route_experts_backward(const void *logits, long long ld, int dtyp
  * device memory of at least moe_decode_sort_slots_workspace() bytes, 256-byte
  * aligned, used until the launches complete (calls that may overlap in time need one
  * each); it need not be cleared, and where that says 0 bytes it is not looked at.
- * T == 0 is a valid no-op that writes nothing. */
+ * T == 0 is a valid no-op that writes nothing: counts, which are then of no slots,
+ * keep what they hold (0 in them before the call makes them right for every T). */
 int moe_decode_sort_slots_workspace(int T, int E, int k, size_t *bytes);
 int moe_decode_sort_slots(const int32_t *topk_ids, const uint8_t *valid, int32_t *counts, int32_t *x_rows,
                           int32_t *positions, void *workspace, size_t workspace_bytes,
@@ -525,7 +528,8 @@ int moe_decode_combine_backward(const void *dy, long long ld_dy, const void *row
  * until the launches complete (calls that may overlap in time need one each); it need
  * not be cleared.
  * Limits: H <= 32768; M < 2^26 up to 1024 columns, 2^24 up to 16384, else 2^22;
- * strides up to 2^30.  M == 0 is a valid no-op that writes nothing. */
+ * strides up to 2^30.  M == 0 is a valid no-op that writes nothing: dweight, whose sums
+ * are then of no rows, keeps what it holds (0 before the call, as for counts above). */
 int moe_decode_rms_norm(const void *x, long long ld_x, const void *residual, long long ld_residual, int dtype,
                         const void *weight, int weight_dtype, float eps, void *y, long long ld_y,
                         uint8_t *q, float *scales, void *sum, long long ld_sum, float *rstd,

@@ -594,7 +594,8 @@ def _workspace(workspace, need, device, stream, where):
 def moe_decode_sort_slots(topk_ids, counts, x_rows, positions, valid=None, workspace=None, stream=None):
     """The slots of topk_ids [T,k] sorted by expert, all int32: counts [E], x_rows [T*k] (the token of each sorted row, as
     moe_decode_matmul_fp8_experts takes it) and positions [T,k] (the sorted row of each slot, as moe_decode_combine takes
-    it); -1 for slots of tokens that are not valid and for ids outside [0,E) (see include/moe_decode.h).
+    it); -1 for slots of tokens that are not valid and for ids outside [0,E) (see include/moe_decode.h).  With no tokens
+    nothing is written, counts neither.
 
     Without a workspace one is taken from torch's allocator for the call (which then runs on the current stream)."""
     L = _load()
@@ -677,7 +678,7 @@ def moe_decode_rms_norm_backward_workspace(M, H):
 def moe_decode_rms_norm_backward(dy, r, weight, rstd, dx, dweight, dsum=None, workspace=None, stream=None):
     """dx [M,H] (the gradient of x and of the residual) and dweight fp32 [H] of moe_decode_rms_norm from dy [M,H], r (its
     sum_out, or x where it had no residual) and rstd; dsum [M,H]: the gradient that reaches sum_out from elsewhere, which
-    may be dx (see include/moe_decode.h).
+    may be dx (see include/moe_decode.h).  With no rows nothing is written, dweight neither.
 
     Without a workspace one is taken from torch's allocator for the call (which then runs on the current stream)."""
     L = _load()

@@ -27,7 +27,8 @@ int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : R <= 12
 // One launch, or three: a workgroup of the one reads all of A of its adapter, and each row of the batch is a workgroup
 // (or sixteen are).  In a graph, us, mixed adapters, one launch against three: R = 16, K = 2048 (N = 4096) 1 row 7.0, 32
 // 7.4 / 12.5, 384 16.1 / 17.4, 512 18.2 / 17.8 and with 16 rows for each adapter 30 / 17; R = 32, K = 1024 384 10.2 / 13.0; R =
-// 64, K = 4096 1 row 22.7 / 14.6, 128 32 / 15.7; R = 128, K = 4096 36 / 18.
+// 64, K = 4096 1 row 22.7 / 14.6, 128 32 / 15.7; R = 128, K = 4096 36 / 18.  The rule does not know the rows' adapters, which
+// the host does not see: with one for all rows (R = 16, K = 2048) 128 rows 12, 256 18, 320 and 384 30, and 385, three launches, 20.
 bool few(int M, int K, int R) {
   const long long a = 16LL * rank_tiles(R) * K;
   return M <= moe::kAdFew && a <= 1 << 17 && M * a <= 3 << 22;

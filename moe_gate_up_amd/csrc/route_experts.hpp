@@ -13,7 +13,10 @@
 // With one (or by sums of two scores) the FP32 values' errors are known; neighbours in the
 // order of choice that lie nearer than those are compared in FP64, one exponential a
 // lane, and a row that this does not settle (or whose groups are as near) is done again
-// in FP64 by the whole wavefront at its end: about one row in 10000 of those measured.
+// in FP64 by the whole wavefront at its end: about one row in 10000 of logits of 1.5 sigma.  Where more than eight experts
+// beyond the choice lie within the error, all rows are: sigmoid scores that saturate and one bias for all, a softmax score
+// that leaves the others nothing, logits of the type's lowest value beside others, a bias of -inf.  262144 tokens of 128
+// experts, top-8, then take 520-640 us (47-53 otherwise), in groups with a bias of -inf 1040; 32 tokens 23-39 (3-4).
 //
 // Vector instructions bound it: 262144 tokens of 128 experts, FP32, sigmoid, bias, 8 groups, the two
 // largest, top-8: 72 us for 151 MB (2.1 TB/s), 424 vector instructions for 4 rows, of them
