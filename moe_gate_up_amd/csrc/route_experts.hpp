@@ -19,9 +19,9 @@
 // experts, top-8, then take 520-640 us (47-53 otherwise), in groups with a bias of -inf 1040; 32 tokens 23-39 (3-4).
 //
 // Vector instructions bound it: 262144 tokens of 128 experts, FP32, sigmoid, bias, 8 groups, the two
-// largest, top-8: 72 us for 151 MB (2.1 TB/s), 424 vector instructions for 4 rows, of them
+// largest, top-8: 71-77 us for 151 MB (2.0 TB/s), 418 vector instructions for 4 rows, of them
 // 96 quarters of an exponential or reciprocal, 120 for the 8 selections and 38 for the sort;
-// without the rows done again 64.  Keys and numbers in two registers and a search for
+// in a graph 64-66.  Keys and numbers in two registers and a search for
 // the lowest number each time took 188.  4 workgroups a CU that go on to the next rows,
 // whose logits are requested ahead; one workgroup for 16 rows 93.  32 tokens of 256 experts: 5.4 us.
 // The gradient: 41 us for 285 MB (6.9 TB/s, some of the logits from the memory-side cache).
